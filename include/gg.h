@@ -529,6 +529,136 @@ gg_status gg_fp8_masked_forward(const void* x, const void* x_scales,
                                 gg_dtype y_dtype, int64_t max_m, int64_t k,
                                 int64_t n, int32_t num_groups, void* stream);
 
+/*
+ * 8-bit rows
+ * ----------
+ * What the operators below call e4m3 rows: one e4m3 byte (OCP E4M3) per
+ * value, and for every row and 128 consecutive values one E8M0 byte (exponent
+ * + 127) at scales[row * (n / 128) + block], dense.  A scale is the smallest
+ * power of two s with amax / s <= 448, 1 for a block of zeros, never below
+ * 2^-126; codes are value / s rounded to nearest even.  amax is taken over
+ * the block's finite values, and an infinity or NaN becomes the NaN code.
+ * gg_fp8_pack_scales takes these scales (src_is_f32 = 0, ld_src = n / 128).
+ * Rounding: a value of a block is off by at most 2^-4 of itself, or 2^-10 s
+ * where it is below 2^-6 s.
+ *
+ * gg_rmsnorm -- the norm in front of the layer, with the residual's addition:
+ *   h = x + residual,  y = h / sqrt(mean(h^2) + eps) * gamma     for each row
+ * in fp32 from the sum to the product, each output rounded once.
+ *   x         [rows, n]  bf16
+ *   residual  [rows, n]  bf16, or NULL for 0
+ *   gamma     [n]        bf16
+ *   h         [rows, n]  bf16 (the residual stream), or NULL; may be x or
+ *                        residual itself
+ *   y         [rows, n]  bf16, or NULL
+ *   y8, y8_scales        e4m3 rows of y (n a multiple of 128), or both NULL
+ * At least one output must be given.  eps >= 0; a row of zeros with eps = 0
+ * gives NaN, as the formula does.
+ *
+ * gg_rmsnorm_grad -- its gradient at h.  With rho = 1 / sqrt(mean(h^2) + eps),
+ * u = h rho and p = dy gamma:
+ *   dx = rho (p - u mean(p u)) + dh,   dgamma = sum over rows of dy u
+ *   dy, h     [rows, n]  bf16 (h as gg_rmsnorm wrote it, or its x if there
+ *                        was no residual)
+ *   dh        [rows, n]  bf16, the gradient that reaches h through the
+ *                        residual stream, or NULL for 0
+ *   dx        [rows, n]  bf16, written: the gradient of x and of residual
+ *                        alike; may be dy or dh itself
+ *   dgamma    [n]        fp32, written (0 for no rows); a fixed order of sums
+ *   workspace            gg_rmsnorm_grad_workspace_bytes(rows, n) bytes of
+ *                        device memory, 16-byte aligned, the caller's; its
+ *                        contents on entry do not matter.  Calls that may
+ *                        overlap need one each.
+ *
+ * gg_fp8_gather_rows -- gg_gather_rows for e4m3 rows with their scales, ready
+ * for gg_fp8_forward on the same offs:
+ *   dst[r] = src[row_slot[r] / topk] for r below the last end offset; zero
+ *   codes and the scale 1 for a padding row; rows past it untouched
+ *   src        [tokens, k]       e4m3 bytes; src_scales [tokens, k / 128]
+ *   dst        [rows_cap, k]
+ *   dst_scales gg_fp8_scale_bytes(GG_FP8_ACT_RAGGED, rows_cap, k, E) bytes,
+ *              16-byte aligned: what gg_fp8_pack_scales would write for the
+ *              gathered rows (tiles past the last one untouched)
+ *
+ * gg_combine_rows_grad -- the gradient of gg_combine_rows on the same
+ * routing:
+ *   dy[slot_row[t * topk + k]] = w[t, k] dout[t]; zero on the padding rows;
+ *   rows at or past the last end offset untouched
+ *   dweights[t, k] = sum_n y[slot_row[t * topk + k], n] dout[t, n] in fp32, 0
+ *   for a dropped slot
+ *   dout      [tokens, n] dout_dtype;  y [rows_cap, n] bf16 (only read for
+ *             dweights; may be NULL without it)
+ *   slot_row, row_slot, offs  as gg_route wrote them, together
+ *   weights   fp32 [tokens, topk], or NULL for 1
+ *   dy        [rows_cap, n] bf16;  dweights fp32 [tokens, topk], or NULL
+ * (The gradient of gg_gather_rows is gg_combine_rows without weights.)
+ *
+ * gg_silu_mul_rows -- SiLU(gate) * up of grouped rows that gg_forward wrote:
+ *   a[i, c] = silu(h[i, c]) * h[i, I + c],  c < I = n / 2, in fp32
+ *   h    [m, n]  bf16, n = 2 I: I gate columns, then I up columns
+ *   a    [m, I]  bf16, or NULL
+ *   a8, a8_scales  e4m3 rows of a, or both NULL
+ *   h8, h8_scales  e4m3 rows of h [m, n], kept for gg_silu_mul_grad, or both
+ *                  NULL
+ * n is a multiple of 16 (of 256 with an e4m3 output).  Only rows an expert
+ * owns are read or written.
+ *
+ * gg_silu_mul_grad -- its gradient, from h or from the kept rows:
+ *   dh[:, c] = da u s (1 + g (1 - s)),  dh[:, I + c] = da g s,
+ *   g = h[:, c], u = h[:, I + c], s = 1 / (1 + exp(-g))
+ *   da   [m, I]  bf16
+ *   h    [m, n]  bf16 with h_scales = NULL, or e4m3 with h_scales [m, n / 128]
+ *   dh   [m, n]  bf16
+ *   act  [m, I]  bf16: silu(g) u formed again (the operand of the next
+ *        projection's weight gradient), or NULL
+ * The masked forms take [E, max_m, ...] and masked_m.
+ *
+ * Errors as the GEMM entry points (pointers 16-byte aligned, scales of any
+ * alignment); all calls are deterministic and safe to capture in a HIP graph.
+ * Cited passages: sglang PR #32385, "Cause" (the quantizer's power-of-two
+ * scale per 128 values between the layer's steps; the SiLU-mul step on the
+ * masked layout); PyTorch issue #152668, "Describe the bug" (the permute
+ * step whose backward these are).
+ */
+gg_status gg_rmsnorm(const void* x, const void* residual, const void* gamma,
+                     void* h, void* y, void* y8, void* y8_scales,
+                     int64_t rows, int64_t n, float eps, void* stream);
+int64_t gg_rmsnorm_grad_workspace_bytes(int64_t rows, int64_t n);
+gg_status gg_rmsnorm_grad(const void* dy, const void* h, const void* gamma,
+                          const void* dh, void* dx, float* dgamma,
+                          void* workspace, int64_t rows, int64_t n, float eps,
+                          void* stream);
+gg_status gg_fp8_gather_rows(const void* src, const void* src_scales,
+                             int64_t tokens, int64_t k,
+                             const int32_t* row_slot, int32_t topk,
+                             const int32_t* offs, int32_t num_groups,
+                             int64_t rows_cap, void* dst, void* dst_scales,
+                             void* stream);
+gg_status gg_combine_rows_grad(const void* dout, gg_dtype dout_dtype,
+                               const void* y, int64_t n,
+                               const int32_t* slot_row,
+                               const int32_t* row_slot, const int32_t* offs,
+                               int32_t num_groups, const float* weights,
+                               int32_t topk, int64_t tokens, int64_t rows_cap,
+                               void* dy, float* dweights, void* stream);
+gg_status gg_silu_mul_rows(const void* h, const int32_t* offs, void* a,
+                           void* a8, void* a8_scales, void* h8,
+                           void* h8_scales, int64_t m, int64_t n,
+                           int32_t num_groups, void* stream);
+gg_status gg_masked_silu_mul_rows(const void* h, const int32_t* masked_m,
+                                  void* a, void* a8, void* a8_scales,
+                                  void* h8, void* h8_scales, int64_t max_m,
+                                  int64_t n, int32_t num_groups, void* stream);
+gg_status gg_silu_mul_grad(const void* da, const void* h,
+                           const void* h_scales, const int32_t* offs, void* dh,
+                           void* act, int64_t m, int64_t n,
+                           int32_t num_groups, void* stream);
+gg_status gg_masked_silu_mul_grad(const void* da, const void* h,
+                                  const void* h_scales,
+                                  const int32_t* masked_m, void* dh, void* act,
+                                  int64_t max_m, int64_t n,
+                                  int32_t num_groups, void* stream);
+
 /* Static description of a status code. */
 const char* gg_status_str(gg_status s);
 

@@ -106,6 +106,20 @@ def load():
         f = getattr(lib, name)
         f.argtypes = [P, P, P, P, P, P, ctypes.c_int, I64, I64, I64, I32, P]
         f.restype = ctypes.c_int
+    F32 = ctypes.c_float
+    lib.gg_rmsnorm.argtypes = [P, P, P, P, P, P, P, I64, I64, F32, P]
+    lib.gg_rmsnorm_grad.argtypes = [P, P, P, P, P, P, P, I64, I64, F32, P]
+    lib.gg_fp8_gather_rows.argtypes = [P, P, I64, I64, P, I32, P, I32, I64, P, P, P]
+    lib.gg_combine_rows_grad.argtypes = [P, ctypes.c_int, P, I64, P, P, P, I32, P, I32, I64, I64, P, P, P]
+    for name in ("gg_silu_mul_rows", "gg_masked_silu_mul_rows"):
+        getattr(lib, name).argtypes = [P, P, P, P, P, P, P, I64, I64, I32, P]
+    for name in ("gg_silu_mul_grad", "gg_masked_silu_mul_grad"):
+        getattr(lib, name).argtypes = [P, P, P, P, P, P, I64, I64, I32, P]
+    for name in ("gg_rmsnorm", "gg_rmsnorm_grad", "gg_fp8_gather_rows", "gg_combine_rows_grad", "gg_silu_mul_rows",
+                 "gg_masked_silu_mul_rows", "gg_silu_mul_grad", "gg_masked_silu_mul_grad"):
+        getattr(lib, name).restype = ctypes.c_int
+    lib.gg_rmsnorm_grad_workspace_bytes.argtypes = [I64, I64]
+    lib.gg_rmsnorm_grad_workspace_bytes.restype = ctypes.c_int64
     lib.gg_status_str.argtypes = [ctypes.c_int]
     lib.gg_status_str.restype = ctypes.c_char_p
     lib.gg_last_error.argtypes = []
@@ -774,3 +788,242 @@ def fp8_masked_forward(x, x_scales, w, w_scales, masked_m, out=None, out_dtype=N
         raise ValueError(f"out must be [{e}, {max_m}, {n}]")
     _fp8_call("gg_fp8_masked_forward", x, x_scales, w, w_scales, masked_m, out, max_m, k, n, e, dev)
     return out
+
+
+# ---------------------------------------------------------------------------
+# norm, 8-bit gather, combine gradient, SiLU-mul rows
+# ---------------------------------------------------------------------------
+
+def _launch(name, dev, *args):
+    """Calls an entry point on ``dev``'s current stream, with ``dev`` current
+    (a kernel goes to the current device)."""
+    torch = _torch()
+    if dev.type != "cuda":
+        raise ValueError(f"{name}: the tensors are on {dev}, expected a GPU")
+    if torch.cuda.current_device() == dev.index:
+        rc = call_raw(name, *args, _stream_handle(dev))
+    else:
+        with torch.cuda.device(dev):
+            rc = call_raw(name, *args, _stream_handle(dev))
+    if rc != 0:
+        raise GGError(name, rc, last_error())
+
+
+def _shaped(t, name, dtype, shape, device):
+    """``t`` checked against a shape, or a new tensor of it."""
+    if t is None:
+        return _torch().empty(shape, dtype=dtype, device=device)
+    _check(t, name, dtype, len(shape), device)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    return t
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _rmsnorm(x, gamma, residual, eps, y, y8, scales, h):
+    torch = _torch()
+    dev = x.device
+    _check(x, "x", torch.bfloat16, 2, dev)
+    rows, n = x.shape
+    _shaped(gamma, "gamma", torch.bfloat16, (n,), dev)
+    if residual is not None:
+        _shaped(residual, "residual", torch.bfloat16, (rows, n), dev)
+        h = _shaped(h, "h_out", torch.bfloat16, (rows, n), dev)
+    elif h is not None:
+        raise ValueError("h_out without a residual: h is x itself")
+    _launch("gg_rmsnorm", dev, _ptr(x), _ptr(residual), _ptr(gamma), _ptr(h), _ptr(y), _ptr(y8), _ptr(scales), rows,
+            n, float(eps))
+    return h
+
+
+def rmsnorm(x, gamma, residual=None, eps=1e-6, out=None, h_out=None):
+    """y = RMSNorm(x + residual) * gamma (gg_rmsnorm): bf16 [rows, n], gamma
+    bf16 [n].  Returns (y, h) with h = x + residual in bf16 (``h_out``, which
+    may be ``residual`` or ``x``), or h = None without a residual."""
+    torch = _torch()
+    y = _shaped(out, "out", torch.bfloat16, tuple(x.shape), x.device)
+    h = _rmsnorm(x, gamma, residual, eps, y, None, None, h_out)
+    return y, h
+
+
+def fp8_rmsnorm(x, gamma, residual=None, eps=1e-6, out=None, out_scales=None, h_out=None, with_bf16=False):
+    """rmsnorm with y as e4m3 rows: uint8 codes [rows, n] and E8M0 bytes
+    [rows, n / 128] (n a multiple of 128).  Returns (codes, scales, h), or
+    (codes, scales, h, y) with the bf16 y too (``with_bf16``)."""
+    torch = _torch()
+    if x.dim() != 2 or x.shape[1] % 128:
+        raise ValueError("x must be [rows, n] with n a multiple of 128")
+    rows, n = x.shape
+    dev = x.device
+    y8 = _shaped(out, "out", torch.uint8, (rows, n), dev)
+    scales = _shaped(out_scales, "out_scales", torch.uint8, (rows, n // 128), dev)
+    y = torch.empty((rows, n), dtype=torch.bfloat16, device=dev) if with_bf16 else None
+    h = _rmsnorm(x, gamma, residual, eps, y, y8, scales, h_out)
+    return (y8, scales, h, y) if with_bf16 else (y8, scales, h)
+
+
+def rmsnorm_grad_workspace_bytes(rows, n) -> int:
+    v = int(load().gg_rmsnorm_grad_workspace_bytes(int(rows), int(n)))
+    if v < 0:
+        raise ValueError("invalid arguments for gg_rmsnorm_grad_workspace_bytes")
+    return v
+
+
+def rmsnorm_grad(dy, h, gamma, dh=None, eps=1e-6, out=None, dgamma=None, workspace=None):
+    """Gradient of rmsnorm at h (gg_rmsnorm_grad): dy, h bf16 [rows, n]; dh:
+    the gradient that reaches h through the residual stream, or None.  Returns
+    (dx bf16 [rows, n] -- of x and of residual alike -- and dgamma fp32 [n])."""
+    torch = _torch()
+    dev = dy.device
+    _check(dy, "dy", torch.bfloat16, 2, dev)
+    rows, n = dy.shape
+    _shaped(h, "h", torch.bfloat16, (rows, n), dev)
+    _shaped(gamma, "gamma", torch.bfloat16, (n,), dev)
+    if dh is not None:
+        _shaped(dh, "dh", torch.bfloat16, (rows, n), dev)
+    dx = _shaped(out, "out", torch.bfloat16, (rows, n), dev)
+    dgamma = _shaped(dgamma, "dgamma", torch.float32, (n,), dev)
+    need = rmsnorm_grad_workspace_bytes(rows, n)
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    _check(workspace, "workspace", torch.uint8, 1, dev)
+    if workspace.numel() < need:
+        raise ValueError(f"workspace must hold {need} bytes")
+    _launch("gg_rmsnorm_grad", dev, _ptr(dy), _ptr(h), _ptr(gamma), _ptr(dh), _ptr(dx), _ptr(dgamma), _ptr(workspace),
+            rows, n, float(eps))
+    return dx, dgamma
+
+
+def fp8_gather_rows(src, scales, row_slot, topk, offs, out=None, out_scales=None):
+    """e4m3 rows and their scales sorted by expert (gg_fp8_gather_rows): src
+    uint8 [tokens, k], scales uint8 E8M0 [tokens, k / 128]; row_slot and offs
+    from ``route``.  Returns (codes [len(row_slot), k], packed scales) as
+    ``fp8_forward`` takes them; rows past offs[-1] are left untouched."""
+    torch = _torch()
+    dev = src.device
+    _check(src, "src", torch.uint8, 2, dev)
+    tokens, k = src.shape
+    if k % 128:
+        raise ValueError("src must be [tokens, k] with k a multiple of 128")
+    _shaped(scales, "scales", torch.uint8, (tokens, k // 128), dev)
+    _check(row_slot, "row_slot", torch.int32, 1, dev)
+    _check(offs, "offs", torch.int32, 1, dev)
+    cap, e = row_slot.shape[0], offs.shape[0]
+    out = _shaped(out, "out", torch.uint8, (cap, k), dev)
+    out_scales = _shaped(out_scales, "out_scales", torch.uint8, (fp8_scale_bytes(GG_FP8_ACT_RAGGED, cap, k, e),), dev)
+    _launch("gg_fp8_gather_rows", dev, _ptr(src), _ptr(scales), tokens, k, _ptr(row_slot), int(topk), _ptr(offs), e,
+            cap, _ptr(out), _ptr(out_scales))
+    return out, out_scales
+
+
+def combine_rows_grad(dout, y, slot_row, row_slot, offs, topk, weights=None, out=None, with_weights=True):
+    """Gradient of combine_rows (gg_combine_rows_grad): dout bf16 or fp32
+    [tokens, n], y bf16 [rows, n] (None without ``with_weights``), and the
+    routing.  Returns (dy bf16 [len(row_slot), n], dweights fp32 [tokens,
+    topk] or None); rows of dy past offs[-1] are left untouched."""
+    torch = _torch()
+    dev = dout.device
+    if dout.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"dout must be bfloat16 or float32, got {dout.dtype}")
+    _check(dout, "dout", dout.dtype, 2, dev)
+    tokens, n = dout.shape
+    topk = int(topk)
+    _shaped(slot_row, "slot_row", torch.int32, (tokens * topk,), dev)
+    _check(row_slot, "row_slot", torch.int32, 1, dev)
+    _check(offs, "offs", torch.int32, 1, dev)
+    cap, e = row_slot.shape[0], offs.shape[0]
+    if weights is not None:
+        _shaped(weights, "weights", torch.float32, (tokens, topk), dev)
+    dw = None
+    if with_weights:
+        if y is None:
+            raise ValueError("the gradient of the weights needs y")
+        _shaped(y, "y", torch.bfloat16, (cap, n), dev)
+        dw = torch.empty((tokens, topk), dtype=torch.float32, device=dev)
+    out = _shaped(out, "out", torch.bfloat16, (cap, n), dev)
+    _launch("gg_combine_rows_grad", dev, _ptr(dout), _dtype_code(dout.dtype), _ptr(y) if with_weights else None, n,
+            _ptr(slot_row), _ptr(row_slot), _ptr(offs), e, _ptr(weights), topk, tokens, cap, _ptr(out), _ptr(dw))
+    return out, dw
+
+
+def _grouped(t, name, dtype, groups, masked):
+    """Checks grouped rows [m, width] or [E, max_m, width]; returns (their
+    leading dimensions, m or max_m, width)."""
+    torch = _torch()
+    _check(t, name, dtype, 3 if masked else 2, t.device)
+    _check(groups, "groups", torch.int32, 1, t.device)
+    if masked and t.shape[0] != groups.shape[0]:
+        raise ValueError(f"{name} and groups must have the same number of experts")
+    return tuple(t.shape[:-1]), t.shape[-2], t.shape[-1]
+
+
+def _silu_mul_rows(h, groups, masked, keep, a, a8, a8s, kept, kept_scales):
+    torch = _torch()
+    lead, m, n = _grouped(h, "h", torch.bfloat16, groups, masked)
+    if keep or kept is not None or kept_scales is not None:
+        if n % 256:
+            raise ValueError("e4m3 rows need I = n / 2 a multiple of 128")
+        kept = _shaped(kept, "kept", torch.uint8, (*lead, n), h.device)
+        kept_scales = _shaped(kept_scales, "kept_scales", torch.uint8, (*lead, n // 128), h.device)
+    _launch("gg_masked_silu_mul_rows" if masked else "gg_silu_mul_rows", h.device, _ptr(h), _ptr(groups), _ptr(a),
+            _ptr(a8), _ptr(a8s), _ptr(kept), _ptr(kept_scales), m, n, groups.shape[0])
+    return () if kept is None else (kept, kept_scales)
+
+
+def silu_mul_rows(h, groups, masked=False, keep=False, out=None, kept=None, kept_scales=None):
+    """a = silu(gate) * up of grouped rows h bf16 [m, 2I] (masked: [E, max_m,
+    2I]; gate columns first), rows an expert owns only (gg_silu_mul_rows).
+    ``keep`` (or a buffer for it) also writes h as e4m3 rows for
+    ``fp8_silu_mul_grad``: returns (a, kept, kept_scales) then, else a."""
+    torch = _torch()
+    if h.shape[-1] % 16:
+        raise ValueError("h must have 2 I columns with I a multiple of 8")
+    a = _shaped(out, "out", torch.bfloat16, (*h.shape[:-1], h.shape[-1] // 2), h.device)
+    kept = _silu_mul_rows(h, groups, masked, keep, a, None, None, kept, kept_scales)
+    return (a, *kept) if kept else a
+
+
+def fp8_silu_mul_rows(h, groups, masked=False, keep=False, out=None, out_scales=None, kept=None, kept_scales=None):
+    """silu_mul_rows with a as e4m3 rows (I a multiple of 128): returns (codes,
+    scales) or (codes, scales, kept, kept_scales)."""
+    torch = _torch()
+    if h.shape[-1] % 256:
+        raise ValueError("e4m3 rows need I = n / 2 a multiple of 128")
+    lead, i = tuple(h.shape[:-1]), h.shape[-1] // 2
+    a8 = _shaped(out, "out", torch.uint8, (*lead, i), h.device)
+    a8s = _shaped(out_scales, "out_scales", torch.uint8, (*lead, i // 128), h.device)
+    return (a8, a8s, *_silu_mul_rows(h, groups, masked, keep, None, a8, a8s, kept, kept_scales))
+
+
+def _silu_mul_grad(da, h, h_scales, groups, masked, with_act, out, act):
+    torch = _torch()
+    lead, m, i = _grouped(da, "da", torch.bfloat16, groups, masked)
+    dev = da.device
+    _shaped(h, "h", torch.bfloat16 if h_scales is None else torch.uint8, (*lead, 2 * i), dev)
+    if h_scales is not None:
+        if i % 128:
+            raise ValueError("e4m3 rows need I a multiple of 128")
+        _shaped(h_scales, "h_scales", torch.uint8, (*lead, 2 * i // 128), dev)
+    dh = _shaped(out, "out", torch.bfloat16, (*lead, 2 * i), dev)
+    if with_act or act is not None:
+        act = _shaped(act, "act", torch.bfloat16, (*lead, i), dev)
+    _launch("gg_masked_silu_mul_grad" if masked else "gg_silu_mul_grad", dev, _ptr(da), _ptr(h), _ptr(h_scales),
+            _ptr(groups), _ptr(dh), _ptr(act), m, 2 * i, groups.shape[0])
+    return dh if act is None else (dh, act)
+
+
+def silu_mul_grad(da, h, groups, masked=False, with_act=False, out=None, act=None):
+    """Gradient of silu_mul_rows (gg_silu_mul_grad): da bf16 [m, I], h bf16
+    [m, 2I] (masked: with a leading E).  Returns dh bf16 [m, 2I], or (dh, a)
+    with the activation formed again (``with_act``, or a buffer for it)."""
+    return _silu_mul_grad(da, h, None, groups, masked, with_act, out, act)
+
+
+def fp8_silu_mul_grad(da, kept, kept_scales, groups, masked=False, with_act=False, out=None, act=None):
+    """silu_mul_grad from the rows ``silu_mul_rows`` kept in 8 bits."""
+    if kept_scales is None:
+        raise ValueError("kept_scales is required")
+    return _silu_mul_grad(da, kept, kept_scales, groups, masked, with_act, out, act)

@@ -598,6 +598,155 @@ gg_status gg_fp8_masked_forward(const void* x, const void* x_scales, const void*
   return fp8_run(true, x, x_scales, w, w_scales, masked_m, y, y_dtype, max_m, k, n, num_groups, stream);
 }
 
+// ---- norm, 8-bit gather, combine gradient, SiLU-mul rows ------------------------------
+
+static gg_status norm_check(int64_t rows, int64_t n, float eps) {
+  if (rows < 0 || rows >= kRowLimit || n < 8 || n % 8 != 0 || n > GG_MAX_KN)
+    return fail(GG_ERR_BAD_DIM, "need 0 <= rows < 2^31 - 2^16 and n a positive multiple of 8 up to GG_MAX_KN");
+  if (!(eps >= 0.0f) || eps > 3.0e38f) return fail(GG_ERR_BAD_DIM, "eps must be a finite number >= 0");
+  return GG_OK;
+}
+
+gg_status gg_rmsnorm(const void* x, const void* residual, const void* gamma, void* h, void* y, void* y8,
+                     void* y8_scales, int64_t rows, int64_t n, float eps, void* stream) {
+  gg_status s = norm_check(rows, n, eps);
+  if (s != GG_OK) return s;
+  if (!gamma || (rows > 0 && (!x || (!h && !y && !y8) || (y8 && !y8_scales))))
+    return fail(GG_ERR_NULL_PTR, "x, gamma, one output and y8's scales are required");
+  if (y8 && n % 128 != 0) return fail(GG_ERR_BAD_DIM, "n must be a multiple of 128 for e4m3 rows");
+  if (!aligned16(x) || !aligned16(residual) || !aligned16(gamma) || !aligned16(h) || !aligned16(y) || !aligned16(y8))
+    return fail(GG_ERR_ALIGNMENT, "pointers must be 16-byte aligned");
+  return hip_result(gg::launch_rmsnorm(x, residual, gamma, h, y, y8, y8 ? y8_scales : nullptr, rows, n, eps,
+                                       static_cast<hipStream_t>(stream)));
+}
+
+int64_t gg_rmsnorm_grad_workspace_bytes(int64_t rows, int64_t n) {
+  if (rows < 0 || rows >= kRowLimit || n < 8 || n % 8 != 0 || n > GG_MAX_KN) return -1;
+  const int64_t g = gg::rmsnorm_grad_groups(rows);
+  return (g > 0 ? g : 1) * n * 4;
+}
+
+gg_status gg_rmsnorm_grad(const void* dy, const void* h, const void* gamma, const void* dh, void* dx, float* dgamma,
+                          void* workspace, int64_t rows, int64_t n, float eps, void* stream) {
+  gg_status s = norm_check(rows, n, eps);
+  if (s != GG_OK) return s;
+  if (!gamma || !dgamma || !workspace || (rows > 0 && (!dy || !h || !dx)))
+    return fail(GG_ERR_NULL_PTR, "a required pointer is NULL");
+  if (!aligned16(dy) || !aligned16(h) || !aligned16(gamma) || !aligned16(dh) || !aligned16(dx) ||
+      !aligned16(workspace) || !aligned4(dgamma))
+    return fail(GG_ERR_ALIGNMENT, "pointers must be 16-byte aligned, dgamma 4-byte aligned");
+  return hip_result(gg::launch_rmsnorm_grad(dy, h, gamma, dh, dx, dgamma, static_cast<float*>(workspace), rows, n, eps,
+                                            static_cast<hipStream_t>(stream)));
+}
+
+gg_status gg_fp8_gather_rows(const void* src, const void* src_scales, int64_t tokens, int64_t k,
+                             const int32_t* row_slot, int32_t topk, const int32_t* offs, int32_t num_groups,
+                             int64_t rows_cap, void* dst, void* dst_scales, void* stream) {
+  if (!offs || (tokens > 0 && (!src || !src_scales)) || (rows_cap > 0 && (!row_slot || !dst || !dst_scales)))
+    return fail(GG_ERR_NULL_PTR, "a required pointer is NULL");
+  if (num_groups < 1 || num_groups > GG_MAX_GROUPS) return fail(GG_ERR_LIMIT, "num_groups must be in [1, GG_MAX_GROUPS]");
+  if (tokens < 0 || rows_cap < 0 || topk < 1 || k < 128 || k % 128 != 0 || k > GG_MAX_KN)
+    return fail(GG_ERR_BAD_DIM,
+                "need tokens, rows_cap >= 0, topk >= 1, k a positive multiple of 128 up to GG_MAX_KN");
+  if (rows_cap >= kRowLimit || tokens >= kRowLimit || tokens * (int64_t)topk >= kRowLimit)
+    return fail(GG_ERR_BAD_DIM, "row and slot counts must be below 2^31 - 2^16");
+  if (!aligned16(src) || !aligned16(dst) || !aligned16(dst_scales) || !aligned4(row_slot) || !aligned4(offs))
+    return fail(GG_ERR_ALIGNMENT, "src, dst and dst_scales must be 16-byte aligned");
+  int cus = 0;
+  gg_status s = device_cus(&cus);
+  if (s != GG_OK) return s;
+  return hip_result(gg::launch_fp8_gather_rows(src, src_scales, row_slot, offs, num_groups, topk, tokens, rows_cap, k,
+                                               dst, dst_scales, cus, static_cast<hipStream_t>(stream)));
+}
+
+gg_status gg_combine_rows_grad(const void* dout, gg_dtype dout_dtype, const void* y, int64_t n,
+                               const int32_t* slot_row, const int32_t* row_slot, const int32_t* offs,
+                               int32_t num_groups, const float* weights, int32_t topk, int64_t tokens,
+                               int64_t rows_cap, void* dy, float* dweights, void* stream) {
+  if (!offs || (tokens > 0 && (!dout || !slot_row)) ||
+      (rows_cap > 0 && (!row_slot || !dy || (tokens > 0 && dweights && !y))))
+    return fail(GG_ERR_NULL_PTR, "a required pointer is NULL");
+  if (dout_dtype != GG_BF16 && dout_dtype != GG_F32)
+    return fail(GG_ERR_BAD_DTYPE, "dout dtype must be GG_BF16 or GG_F32");
+  if (num_groups < 1 || num_groups > GG_MAX_GROUPS) return fail(GG_ERR_LIMIT, "num_groups must be in [1, GG_MAX_GROUPS]");
+  if (n < 8 || n % 8 != 0 || n > GG_MAX_KN || tokens < 0 || topk < 1 || rows_cap < 0)
+    return fail(GG_ERR_BAD_DIM, "need n a positive multiple of 8 up to GG_MAX_KN, tokens, rows_cap >= 0, topk >= 1");
+  if (rows_cap >= kRowLimit || tokens >= kRowLimit || tokens * (int64_t)topk >= kRowLimit)
+    return fail(GG_ERR_BAD_DIM, "row and slot counts must be below 2^31 - 2^16");
+  if (!aligned16(dout) || !aligned16(y) || !aligned16(dy) || !aligned4(slot_row) || !aligned4(row_slot) ||
+      !aligned4(offs) || !aligned4(weights) || !aligned4(dweights))
+    return fail(GG_ERR_ALIGNMENT, "dout, y and dy must be 16-byte aligned");
+  int cus = 0;
+  gg_status s = device_cus(&cus);
+  if (s != GG_OK) return s;
+  return hip_result(gg::launch_combine_rows_grad(dout, dout_dtype == GG_F32, dweights ? y : nullptr, slot_row,
+                                                 row_slot, offs, num_groups, weights, topk, tokens, rows_cap, n, dy,
+                                                 dweights, cus, static_cast<hipStream_t>(stream)));
+}
+
+// n = 2 I; eight: an e4m3 operand or output is among the arguments.
+static gg_status silu_check(const int32_t* groups, int64_t m, int64_t n, int32_t E, bool masked, bool eight) {
+  if (!groups) return fail(GG_ERR_NULL_PTR, "a required pointer is NULL");
+  if (E < 1 || E > GG_MAX_GROUPS) return fail(GG_ERR_LIMIT, "num_groups must be in [1, GG_MAX_GROUPS]");
+  if (m < 0 || n < 16 || n % 16 != 0 || n > GG_MAX_KN)
+    return fail(GG_ERR_BAD_DIM, "need rows >= 0 and n (= 2 I) a positive multiple of 16 up to GG_MAX_KN");
+  if (eight && n % 256 != 0) return fail(GG_ERR_BAD_DIM, "n (= 2 I) must be a multiple of 256 for e4m3 rows");
+  if (m >= kRowLimit) return fail(GG_ERR_BAD_DIM, "row count must be below 2^31 - 2^16");
+  if (masked) return masked_rows(m, E);
+  return GG_OK;
+}
+
+static gg_status silu_run(bool masked, const void* h, const int32_t* groups, void* a, void* a8, void* a8_scales,
+                          void* h8, void* h8_scales, int64_t m, int64_t n, int32_t E, void* stream) {
+  gg_status s = silu_check(groups, m, n, E, masked, a8 || h8);
+  if (s != GG_OK) return s;
+  if (m > 0 && (!h || (!a && !a8 && !h8) || (a8 && !a8_scales) || (h8 && !h8_scales)))
+    return fail(GG_ERR_NULL_PTR, "h, one output and the scales of e4m3 outputs are required");
+  if (!aligned16(h) || !aligned16(a) || !aligned16(a8) || !aligned16(h8) || !aligned4(groups))
+    return fail(GG_ERR_ALIGNMENT, "pointers must be 16-byte aligned");
+  int cus = 0;
+  s = device_cus(&cus);
+  if (s != GG_OK) return s;
+  return hip_result(gg::launch_silu_mul_rows(masked, h, groups, E, m, n / 2, a, a8, a8_scales, h8, h8_scales, cus,
+                                             static_cast<hipStream_t>(stream)));
+}
+
+gg_status gg_silu_mul_rows(const void* h, const int32_t* offs, void* a, void* a8, void* a8_scales, void* h8,
+                           void* h8_scales, int64_t m, int64_t n, int32_t num_groups, void* stream) {
+  return silu_run(false, h, offs, a, a8, a8_scales, h8, h8_scales, m, n, num_groups, stream);
+}
+
+gg_status gg_masked_silu_mul_rows(const void* h, const int32_t* masked_m, void* a, void* a8, void* a8_scales,
+                                  void* h8, void* h8_scales, int64_t max_m, int64_t n, int32_t num_groups,
+                                  void* stream) {
+  return silu_run(true, h, masked_m, a, a8, a8_scales, h8, h8_scales, max_m, n, num_groups, stream);
+}
+
+static gg_status silu_grad_run(bool masked, const void* da, const void* h, const void* h_scales,
+                               const int32_t* groups, void* dh, void* act, int64_t m, int64_t n, int32_t E,
+                               void* stream) {
+  gg_status s = silu_check(groups, m, n, E, masked, h_scales != nullptr);
+  if (s != GG_OK) return s;
+  if (m > 0 && (!da || !h || !dh)) return fail(GG_ERR_NULL_PTR, "a required pointer is NULL");
+  if (!aligned16(da) || !aligned16(h) || !aligned16(dh) || !aligned16(act) || !aligned4(groups))
+    return fail(GG_ERR_ALIGNMENT, "pointers must be 16-byte aligned");
+  int cus = 0;
+  s = device_cus(&cus);
+  if (s != GG_OK) return s;
+  return hip_result(gg::launch_silu_mul_grad(masked, da, h, h_scales, groups, E, m, n / 2, dh, act, cus,
+                                             static_cast<hipStream_t>(stream)));
+}
+
+gg_status gg_silu_mul_grad(const void* da, const void* h, const void* h_scales, const int32_t* offs, void* dh,
+                           void* act, int64_t m, int64_t n, int32_t num_groups, void* stream) {
+  return silu_grad_run(false, da, h, h_scales, offs, dh, act, m, n, num_groups, stream);
+}
+
+gg_status gg_masked_silu_mul_grad(const void* da, const void* h, const void* h_scales, const int32_t* masked_m,
+                                  void* dh, void* act, int64_t max_m, int64_t n, int32_t num_groups, void* stream) {
+  return silu_grad_run(true, da, h, h_scales, masked_m, dh, act, max_m, n, num_groups, stream);
+}
+
 const char* gg_status_str(gg_status s) {
   switch (s) {
     case GG_OK: return "GG_OK";

@@ -87,4 +87,34 @@ hipError_t launch_dbias(bool masked, const void* dy, const int32_t* groups, cons
                         int64_t n, int32_t E, float* dbias, hipStream_t stream);
 hipError_t launch_dscale(bool masked, const void* dy, const int32_t* groups, const void* bias, int64_t m,
                          int64_t n, int32_t E, float* ds, int num_cus, hipStream_t stream);
+
+// Norm with the residual's addition and its gradient (gg_norm.hip).  Null:
+// res, h, y, y8 with scales; dh.  part holds rmsnorm_grad_groups(rows) rows of
+// n floats.
+int64_t rmsnorm_grad_groups(int64_t rows);
+hipError_t launch_rmsnorm(const void* x, const void* res, const void* gamma, void* h, void* y, void* y8,
+                          void* scales, int64_t rows, int64_t n, float eps, hipStream_t stream);
+hipError_t launch_rmsnorm_grad(const void* dy, const void* h, const void* gamma, const void* dh, void* dx,
+                               float* dgamma, float* part, int64_t rows, int64_t n, float eps, hipStream_t stream);
+
+// e4m3 rows and their scales sorted by expert (gg_fp8_gather.hip).
+hipError_t launch_fp8_gather_rows(const void* src, const void* src_scales, const int32_t* row_slot,
+                                  const int32_t* offs, int32_t E, int32_t topk, int64_t tokens, int64_t rows_cap,
+                                  int64_t k, void* dst, void* dst_scales, int num_cus, hipStream_t stream);
+
+// Gradient of combine_rows (gg_combine_grad.hip).  Null: w; y with dw.
+hipError_t launch_combine_rows_grad(const void* dout, bool dout_f32, const void* y, const int32_t* slot_row,
+                                    const int32_t* row_slot, const int32_t* offs, int32_t E, const float* w,
+                                    int32_t topk, int64_t tokens, int64_t rows_cap, int64_t n, void* dy, float* dw,
+                                    int num_cus, hipStream_t stream);
+
+// SiLU-mul on grouped rows of 2 width values and its gradient
+// (gg_silu_rows.hip).  Null: a; a8, h8 with their scales; act.  h is e4m3
+// where h_scales is given, bf16 where it is null.
+hipError_t launch_silu_mul_rows(bool masked, const void* h, const int32_t* groups, int32_t E, int64_t m,
+                                int64_t width, void* a, void* a8, void* a8_scales, void* h8, void* h8_scales,
+                                int num_cus, hipStream_t stream);
+hipError_t launch_silu_mul_grad(bool masked, const void* da, const void* h, const void* h_scales,
+                                const int32_t* groups, int32_t E, int64_t m, int64_t width, void* dh, void* act,
+                                int num_cus, hipStream_t stream);
 }  // namespace gg
