@@ -530,6 +530,34 @@ gg_status gg_fp8_masked_forward(const void* x, const void* x_scales,
                                 int64_t n, int32_t num_groups, void* stream);
 
 /*
+ * gg_fp8_wgrad -- the weight gradient from activations kept in 8 bits: the
+ * operand pair that gg_fp8_forward read is all a training step keeps of X.
+ *   dW[g] = alpha * Xhat[rows of g]^T . dY[rows of g] + beta * dW[g],
+ *   Xhat[i, c] = x[i, c] * sx[i, c / 128]
+ *   x         [m, k]     e4m3 bytes, k a multiple of 128
+ *   x_scales  packed (GG_FP8_ACT_RAGGED, same offs)
+ *   dy        [m, n]     bf16
+ *   dw        [E, k, n]  dw_dtype, as gg_wgrad_ex
+ * Xhat enters the matrix instructions as bf16, which holds it exactly while
+ * its scale is at least 2^-117; otherwise as gg_wgrad_ex.  A scale byte of 0
+ * counts as 0 here.
+ * gg_fp8_masked_wgrad -- the same on the masked layout: x [E, max_m, k],
+ * x_scales packed with GG_FP8_ACT_MASKED and the same masked_m.
+ * Cited passages: sglang PR #32385, "Cause" (the fp8 operands and their
+ * scales); TransformerEngine PR #3542, "Changes" (overwrite and accumulating
+ * wgrad).
+ */
+gg_status gg_fp8_wgrad(const void* x, const void* x_scales, const void* dy,
+                       const int32_t* offs, void* dw, gg_dtype dw_dtype,
+                       int64_t m, int64_t k, int64_t n, int32_t num_groups,
+                       float alpha, float beta, void* stream);
+gg_status gg_fp8_masked_wgrad(const void* x, const void* x_scales,
+                              const void* dy, const int32_t* masked_m,
+                              void* dw, gg_dtype dw_dtype, int64_t max_m,
+                              int64_t k, int64_t n, int32_t num_groups,
+                              float alpha, float beta, void* stream);
+
+/*
  * 8-bit rows
  * ----------
  * What the operators below call e4m3 rows: one e4m3 byte (OCP E4M3) per

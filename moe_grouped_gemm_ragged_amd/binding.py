@@ -107,6 +107,10 @@ def load():
         f.argtypes = [P, P, P, P, P, P, ctypes.c_int, I64, I64, I64, I32, P]
         f.restype = ctypes.c_int
     F32 = ctypes.c_float
+    for name in ("gg_fp8_wgrad", "gg_fp8_masked_wgrad"):
+        f = getattr(lib, name)
+        f.argtypes = [P, P, P, P, P, ctypes.c_int, I64, I64, I64, I32, F32, F32, P]
+        f.restype = ctypes.c_int
     lib.gg_rmsnorm.argtypes = [P, P, P, P, P, P, P, I64, I64, F32, P]
     lib.gg_rmsnorm_grad.argtypes = [P, P, P, P, P, P, P, I64, I64, F32, P]
     lib.gg_fp8_gather_rows.argtypes = [P, P, I64, I64, P, I32, P, I32, I64, P, P, P]
@@ -1027,3 +1031,42 @@ def fp8_silu_mul_grad(da, kept, kept_scales, groups, masked=False, with_act=Fals
     if kept_scales is None:
         raise ValueError("kept_scales is required")
     return _silu_mul_grad(da, kept, kept_scales, groups, masked, with_act, out, act)
+
+
+# ---------------------------------------------------------------------------
+# weight gradient from e4m3 activations
+# ---------------------------------------------------------------------------
+
+def _fp8_wgrad(name, layout, x, x_scales, dy, groups, out, out_dtype, alpha, beta):
+    torch = _torch()
+    _need_out(out, beta)
+    masked = layout == GG_FP8_ACT_MASKED
+    lead, m, k = _grouped(x, "x", torch.uint8, groups, masked)
+    dev = x.device
+    _check(dy, "dy", torch.bfloat16, len(lead) + 1, dev)
+    if tuple(dy.shape[:-1]) != lead:
+        raise ValueError("x and dy must have the same rows")
+    if k % 128:
+        raise ValueError("x must have a multiple of 128 columns")
+    e, n = groups.shape[0], dy.shape[-1]
+    _check(x_scales, "x_scales", torch.uint8, 1, dev)
+    if x_scales.numel() < fp8_scale_bytes(layout, m, k, e):
+        raise ValueError("packed scales are smaller than fp8_scale_bytes requires")
+    out = _shaped(out, "out", (out_dtype or torch.float32) if out is None else out.dtype, (e, k, n), dev)
+    _launch(name, dev, _ptr(x), _ptr(x_scales), _ptr(dy), _ptr(groups), _ptr(out), _dtype_code(out.dtype), m, k, n, e,
+            float(alpha), float(beta))
+    return out
+
+
+def fp8_wgrad(x, x_scales, dy, offs, out=None, out_dtype=None, alpha=1.0, beta=0.0):
+    """dW[g] = (x sx)[rows of g]^T . dY[rows of g] (gg_fp8_wgrad) from the
+    operand pair of ``fp8_forward``: x uint8 e4m3 [m, k], x_scales packed
+    (GG_FP8_ACT_RAGGED, same offs); dy bf16 [m, n].  All of ``out`` [E, k, n]
+    (fp32 unless said otherwise) is written; alpha / beta as in wgrad."""
+    return _fp8_wgrad("gg_fp8_wgrad", GG_FP8_ACT_RAGGED, x, x_scales, dy, offs, out, out_dtype, alpha, beta)
+
+
+def fp8_masked_wgrad(x, x_scales, dy, masked_m, out=None, out_dtype=None, alpha=1.0, beta=0.0):
+    """fp8_wgrad on the masked layout: x uint8 [E, max_m, k], x_scales packed
+    with GG_FP8_ACT_MASKED and the same masked_m; dy bf16 [E, max_m, n]."""
+    return _fp8_wgrad("gg_fp8_masked_wgrad", GG_FP8_ACT_MASKED, x, x_scales, dy, masked_m, out, out_dtype, alpha, beta)

@@ -598,6 +598,37 @@ gg_status gg_fp8_masked_forward(const void* x, const void* x_scales, const void*
   return fp8_run(true, x, x_scales, w, w_scales, masked_m, y, y_dtype, max_m, k, n, num_groups, stream);
 }
 
+static gg_status fp8_wgrad_run(bool masked, const void* x, const void* xs, const void* dy, const int32_t* groups,
+                               void* dw, gg_dtype dw_dtype, int64_t rows, int64_t k, int64_t n, int32_t num_groups,
+                               float alpha, float beta, void* stream) {
+  gg_status s = check(x, dy, groups, dw, dw_dtype, rows, k, n, num_groups);
+  if (s != GG_OK) return s;
+  if (!xs) return fail(GG_ERR_NULL_PTR, "a required pointer is NULL");
+  if (k % 128 != 0) return fail(GG_ERR_BAD_DIM, "k must be a multiple of 128 (one scale per 128 values)");
+  if (!aligned16(xs)) return fail(GG_ERR_ALIGNMENT, "pointers must be 16-byte aligned");
+  if (masked) {
+    s = masked_rows(rows, num_groups);
+    if (s != GG_OK) return s;
+  }
+  int cus = 0;
+  s = device_cus(&cus);
+  if (s != GG_OK) return s;
+  return hip_result(gg::launch_fp8_wgrad(masked, x, xs, dy, groups, dw, dw_dtype == GG_F32, rows, k, n, num_groups,
+                                         alpha, beta, cus, static_cast<hipStream_t>(stream)));
+}
+
+gg_status gg_fp8_wgrad(const void* x, const void* x_scales, const void* dy, const int32_t* offs, void* dw,
+                       gg_dtype dw_dtype, int64_t m, int64_t k, int64_t n, int32_t num_groups, float alpha,
+                       float beta, void* stream) {
+  return fp8_wgrad_run(false, x, x_scales, dy, offs, dw, dw_dtype, m, k, n, num_groups, alpha, beta, stream);
+}
+
+gg_status gg_fp8_masked_wgrad(const void* x, const void* x_scales, const void* dy, const int32_t* masked_m, void* dw,
+                              gg_dtype dw_dtype, int64_t max_m, int64_t k, int64_t n, int32_t num_groups,
+                              float alpha, float beta, void* stream) {
+  return fp8_wgrad_run(true, x, x_scales, dy, masked_m, dw, dw_dtype, max_m, k, n, num_groups, alpha, beta, stream);
+}
+
 // ---- norm, 8-bit gather, combine gradient, SiLU-mul rows ------------------------------
 
 static gg_status norm_check(int64_t rows, int64_t n, float eps) {

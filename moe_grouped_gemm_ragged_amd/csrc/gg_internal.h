@@ -53,6 +53,13 @@ hipError_t launch_fp8(bool masked, const void* x, const void* sx, const void* w,
                       const int32_t* groups, void* c, bool out_f32, int64_t m, int64_t k, int64_t n,
                       int32_t num_groups, int num_cus, hipStream_t stream);
 
+// The weight gradient from e4m3 activations: x [rows, k] e4m3 with scales sx
+// in the packed layout, dy bf16, dw[g] = alpha * x^T dy + beta * dw[g].
+// Arguments were validated by the caller.
+hipError_t launch_fp8_wgrad(bool masked, const void* x, const void* sx, const void* dy, const int32_t* groups,
+                            void* dw, bool out_f32, int64_t m, int64_t k, int64_t n, int32_t num_groups, float alpha,
+                            float beta, int num_cus, hipStream_t stream);
+
 // Packed fp8 scale tiles for `rows` rows of an operand: layout 0 ragged
 // activations (an upper bound: ceil(rows / 256) + num_groups), 1 masked
 // activations and 2 weights (num_groups * ceil(rows / 256)).  Each tile

@@ -13,6 +13,7 @@
 //   masked wgrad   k x n                  active rows  X[e] (red-strided) dY[e](red-strided)
 //   SiLU fwd       as forward, 128 activation columns from a gate/up panel
 //   fp8 fwd        expert rows x n        k            X e4m3 (contig)    W[g] [n, k] e4m3 (contig)
+//   fp8 wgrad      k x n                  expert rows  X e4m3 (strided)   dY   (red-strided)
 //
 // (The [E, N, K] weight layout of the bf16 passes is these modes with the
 // dimensions exchanged; the host entry points do the mapping.)  Epilogues:
@@ -97,7 +98,7 @@ typedef short shortx4 __attribute__((ext_vector_type(4)));
 
 enum Mode {
   FWD = 0, DGRAD = 1, WGRAD = 2, MASKED = 3, MASKED_DGRAD = 4, MASKED_WGRAD = 5,
-  FWD_SILU = 6, MASKED_SILU = 7, FP8 = 8, FP8_MASKED = 9
+  FWD_SILU = 6, MASKED_SILU = 7, FP8 = 8, FP8_MASKED = 9, FP8_WGRAD = 10, FP8_MASKED_WGRAD = 11
 };
 
 // The masked modes are the ragged passes on the masked layout: expert e's
@@ -105,13 +106,16 @@ enum Mode {
 // modes are forwards whose epilogue applies the gate/up activation.
 constexpr bool is_masked(int mode) {
   return mode == MASKED || mode == MASKED_DGRAD || mode == MASKED_WGRAD || mode == MASKED_SILU ||
-         mode == FP8_MASKED;
+         mode == FP8_MASKED || mode == FP8_MASKED_WGRAD;
 }
-// The fp8 modes: e4m3 operands, X [rows, K] and W [E, N, K] (both
+// The fp8 forward modes: e4m3 operands, X [rows, K] and W [E, N, K] (both
 // reduction-contiguous), one power-of-two scale per 128 reduction values.
 constexpr bool is_fp8(int mode) { return mode == FP8 || mode == FP8_MASKED; }
+// The fp8 wgrad modes: X [rows, K] e4m3 with one power-of-two scale per row
+// and 128 columns, dY bf16.
+constexpr bool is_x8(int mode) { return mode == FP8_WGRAD || mode == FP8_MASKED_WGRAD; }
 constexpr bool is_silu(int mode) { return mode == FWD_SILU || mode == MASKED_SILU; }
-constexpr bool is_wgrad(int mode) { return mode == WGRAD || mode == MASKED_WGRAD; }
+constexpr bool is_wgrad(int mode) { return mode == WGRAD || mode == MASKED_WGRAD || is_x8(mode); }
 constexpr bool is_dgrad(int mode) { return mode == DGRAD || mode == MASKED_DGRAD; }
 
 struct Params {
@@ -532,6 +536,217 @@ __device__ __attribute__((always_inline)) inline void mainloop_pp(
       if (kt + 1 < nk) GG_PP_STAGE1(s1, s2, s0, kt + 1)
       if (kt + 2 < nk) GG_PP_STAGE1(s2, s3, s1, kt + 2)
       if (kt + 3 < nk) GG_PP_STAGE1(s3, s0, s2, kt + 3)
+    }
+#undef GG_PP_STAGE1
+  }
+#undef GG_PP_READ
+#undef GG_PP_MFMA
+}
+
+// ---- ping-pong main loop with an e4m3 A operand (fp8 wgrad) -------------------------
+//
+// The wgrad schedule above with X as e4m3 rows and one power-of-two scale per
+// row and 128 columns.  A scale belongs to a reduction row of the A tile, so
+// it cannot go into a matrix instruction's block scale (that runs along the
+// reduction); instead X becomes bf16 on its way into LDS -- exactly: an e4m3
+// value has 4 significant bits and the scale only moves its exponent -- and
+// fragments and MFMAs are those of the bf16 wgrad.  So group 0 moves A through
+// registers: two 16-byte loads per lane and stage (half the bytes of bf16),
+// converted 16 columns at a time (one scale each) and written to LDS in the
+// red-strided layout.  Its step 2s + 1 reads the fragments of stage s + 1,
+// converts and writes A of stage s + 2 and loads A of stage s + 4 into the
+// registers that frees: 4 steps from load to use, and the write is two
+// barriers ahead of its first reader.  Group 1 is the bf16 schedule's.
+
+// A of two stages on its way, and the scales of their 128 reduction rows: a
+// dword for each of this lane's two rows of a stage (16 jj + lane / 4), byte
+// s mod 4 for stage s.
+struct X8Regs {
+  u32x4 even[2], odd[2];
+  uint32_t sc[2];
+};
+
+// Load jj of wave w covers reduction rows 16 jj .. + 15 of tile columns 64 w
+// .. + 63: lane i row 16 jj + i / 4, columns 16 (i mod 4) .. + 15.  Rows past
+// the expert's last one read as zero; columns past k belong to tile rows that
+// are not stored.
+template <bool WIDE>
+__device__ __forceinline__ void x8_load(const Operand& op, int q0, int lane_in, int w, u32x4 (&r)[2]) {
+  const int lane = (int)opaque_v((uint32_t)lane_in);
+  const int left = op.red - q0;
+  int last = left - 1;
+  if constexpr (WIDE) last = last < 63 ? last : 63;
+  const uint32_t nrec = left > 0 ? (uint32_t)last * op.ld_bytes + op.row_tail : 0u;
+  const __amdgpu_buffer_rsrc_t rs = make_rsrc(op.origin + (int64_t)q0 * op.ld_bytes, nrec);
+  const uint32_t voff = (uint32_t)(lane >> 2) * op.ld_bytes + (uint32_t)(64 * w + 16 * (lane & 3));
+#pragma unroll
+  for (int jj = 0; jj < 2; ++jj)
+    r[jj] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                                          rs, voff + (uint32_t)(16 * jj) * op.ld_bytes, 0, 0));
+}
+
+// Scale dwords of reduction rows q0 .. q0 + 127 (q0 a multiple of 128): sa
+// is the packed tile of the expert's first 256 rows, from the k-block of the
+// tile's first column on; tile_bytes a packed tile's bytes, left those from
+// that k-block to its end (a tile's last columns may have no k-block).
+__device__ __forceinline__ void x8_scales(const uint8_t* sa, int64_t tile_bytes, uint32_t left, int q0, int red,
+                                          int lane_in, int w, uint32_t (&sc)[2]) {
+  const int lane = (int)opaque_v((uint32_t)lane_in);
+  const __amdgpu_buffer_rsrc_t rs = make_rsrc(sa + (int64_t)(q0 >> 8) * tile_bytes, q0 < red ? left : 0u);
+  const uint32_t voff = (uint32_t)(256 * (w >> 1) + ((q0 >> 7) & 1) * 128 + 4 * (lane >> 2));
+#pragma unroll
+  for (int jj = 0; jj < 2; ++jj) sc[jj] = __builtin_amdgcn_raw_buffer_load_b32(rs, voff + 64 * jj, 0, 0);
+}
+
+// Converts a stage and writes it to its A region; byte: the stage's byte of
+// the scale dwords.
+__device__ __forceinline__ void x8_write(const u32x4 (&r)[2], const uint32_t (&sc)[2], int byte, int lane_in, int w,
+                                         uint8_t* lds_op) {
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  const int lane = (int)opaque_v((uint32_t)lane_in);
+#pragma unroll
+  for (int jj = 0; jj < 2; ++jj) {
+    const float scale = __builtin_bit_cast(float, ((sc[jj] >> (8 * byte)) & 0xFFu) << 23);
+    const int q = 16 * jj + (lane >> 2);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      u32x4 o;
+#pragma unroll
+      for (int d = 0; d < 2; ++d) {
+        const bf16x2 lo = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(r[jj][2 * e + d], scale, false);
+        const bf16x2 hi = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(r[jj][2 * e + d], scale, true);
+        o[2 * d] = __builtin_bit_cast(uint32_t, lo);
+        o[2 * d + 1] = __builtin_bit_cast(uint32_t, hi);
+      }
+      const int chunk = (2 * (lane & 3) + e) ^ (4 * ((q >> 1) & 1));
+      *reinterpret_cast<u32x4*>(lds_op + 4096 * w + 128 * q + 16 * chunk) = o;
+    }
+  }
+}
+
+// Loads in flight when the loop starts: group 0 A of stages 0 and 1 and the
+// scales of the first 128 rows (registers), group 1 B of stages 0..2.
+template <bool WIDE>
+__device__ __attribute__((always_inline)) inline void prologue_loads_x8(
+    uint8_t* __restrict__ s0, uint8_t* __restrict__ s1, uint8_t* __restrict__ s2, const uint8_t* __restrict__ a_origin,
+    const uint8_t* __restrict__ b_origin, const uint8_t* __restrict__ sa, int64_t tile_bytes, uint32_t sc_left,
+    Operand A, Operand B, int tid, int wave, X8Regs& x) {
+  A.origin = a_origin;
+  B.origin = b_origin;
+  const int lane = tid & 63;
+  const int w = wave & 3;
+  if (wave < 4) {
+    x8_scales(sa, tile_bytes, sc_left, 0, A.red, lane, w, x.sc);
+    x8_load<WIDE>(A, 0, lane, w, x.even);
+    x8_load<WIDE>(A, BK, lane, w, x.odd);
+  } else {
+#define GG_PP_PRO(S, BUF)                                                   \
+    {                                                                       \
+      const DmaCtx c = dma_ctx_grp<true, WIDE>(B, (S) * BK, lane, w);       \
+      _Pragma("unroll") for (int jj = 0; jj < 4; ++jj) dma_load_grp(c, (BUF) + OP_BYTES, w, jj); \
+    }
+    GG_PP_PRO(0, s0) GG_PP_PRO(1, s1) GG_PP_PRO(2, s2)
+#undef GG_PP_PRO
+  }
+}
+
+template <bool WIDE>
+__device__ __attribute__((always_inline)) inline void mainloop_x8(
+    uint8_t* __restrict__ s0, uint8_t* __restrict__ s1, uint8_t* __restrict__ s2, uint8_t* __restrict__ s3,
+    const uint8_t* __restrict__ a_origin, const uint8_t* __restrict__ b_origin, const uint8_t* __restrict__ sa,
+    int64_t tile_bytes, uint32_t sc_left, Operand A, Operand B, int tid, int wave, const FragAddr& faa,
+    const FragAddr& fab, floatx16 (&acc)[TM][TN], int prev_stores, X8Regs& x) {
+  A.origin = a_origin;
+  B.origin = b_origin;
+  const int nk = (A.red + BK - 1) / BK;
+  if (nk <= 0) return;
+  const int lane = tid & 63;
+  const int w = wave & 3;
+  const bool g0 = wave < 4;
+  const Regions rg = {{s0, s1, s2, s3, s0 + OP_BYTES, s1 + OP_BYTES, s2 + OP_BYTES, s3 + OP_BYTES}};
+  pp_regions_escape(rg);
+  Frags f0, f1;
+#define GG_PP_MFMA()                                                                              \
+  {                                                                                               \
+    _Pragma("unroll") for (int q = 0; q < TM * TN; ++q) {                                         \
+      const int i = q / TN, j = q % TN;                                                           \
+      acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f0.b[j], f0.a[i], acc[i][j], 0, 0, 0); \
+    }                                                                                             \
+    _Pragma("unroll") for (int q = 0; q < TM * TN; ++q) {                                         \
+      const int i = q / TN, j = q % TN;                                                           \
+      acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f1.b[j], f1.a[i], acc[i][j], 0, 0, 0); \
+    }                                                                                             \
+    mfma_fence(acc);                                                                              \
+  }
+#define GG_PP_READ(BUF)                                                                           \
+  {                                                                                               \
+    read_stage_frags<true, true, TM>(BUF, (BUF) + OP_BYTES, faa, fab, 0, f0);                     \
+    read_stage_frags<true, true, TM>(BUF, (BUF) + OP_BYTES, faa, fab, 1, f1);                     \
+  }
+  if (g0) {
+    uint32_t next[2];
+    x8_write(x.even, x.sc, 0, lane, w, s0);
+    x8_load<WIDE>(A, 2 * BK, lane, w, x.even);
+    x8_write(x.odd, x.sc, 1, lane, w, s1);
+    x8_load<WIDE>(A, 3 * BK, lane, w, x.odd);
+    pp_sync<kNoVm>(rg);                              // A of stages 0, 1 written, B of stage 0 landed
+    GG_PP_READ(s0)
+  // BN: the slot of stage KT + 1, BW: of KT + 2; R: the registers of stage
+  // KT + 2, whose scales are byte BYTE of SC
+#define GG_PP_STAGE0(BN, BW, R, SC, BYTE, KT)                                                     \
+  {                                                                                               \
+    __builtin_amdgcn_sched_barrier(0);                                                            \
+    GG_PP_MFMA()                                     /* step 2 KT: compute stage KT */            \
+    __builtin_amdgcn_sched_barrier(0);                                                            \
+    pp_sync<kNoVm>(rg);                              /* B of stage KT + 1 landed */               \
+    __builtin_amdgcn_sched_barrier(0);                                                            \
+    if ((KT) + 1 < nk) GG_PP_READ(BN)                /* step 2 KT + 1: read stage KT + 1 */       \
+    x8_write(R, SC, BYTE, lane, w, BW);                                                           \
+    x8_load<WIDE>(A, ((KT) + 4) * BK, lane, w, R);                                                \
+    __builtin_amdgcn_sched_barrier(0);                                                            \
+    pp_sync<kNoVm>(rg);                              /* fragments in registers, A written */      \
+  }
+    for (int kt = 0; kt < nk; kt += 4) {
+      x8_scales(sa, tile_bytes, sc_left, (kt + 4) * BK, A.red, lane, w, next);
+      GG_PP_STAGE0(s1, s2, x.even, x.sc, 2, kt)
+      // (leaving the loop, rather than skipping a stage and going on: a path
+      // on which the next stage comes without the loads of this one would make
+      // the compiler wait for loads that are still wanted in flight)
+      if (kt + 1 >= nk) break;
+      GG_PP_STAGE0(s2, s3, x.odd, x.sc, 3, kt + 1)
+      if (kt + 2 >= nk) break;
+      GG_PP_STAGE0(s3, s0, x.even, next, 0, kt + 2)
+      if (kt + 3 >= nk) break;
+      GG_PP_STAGE0(s0, s1, x.odd, next, 1, kt + 3)
+      x.sc[0] = next[0];
+      x.sc[1] = next[1];
+    }
+#undef GG_PP_STAGE0
+  } else {
+    // stage 0 of B landed (stages 1, 2 in flight, and the previous tile's
+    // stores where they went out behind these loads)
+    if (prev_stores == stores_f32<TM>()) pp_sync<8 + stores_f32<TM>()>(rg);
+    else pp_sync<8>(rg);
+#define GG_PP_STAGE1(BC, BP, KT)                                                                  \
+  {                                                                                               \
+    __builtin_amdgcn_sched_barrier(0);                                                            \
+    GG_PP_READ(BC)                                   /* step 2 KT: read stage KT */               \
+    {                                                                                             \
+      const DmaCtx cb = dma_ctx_grp<true, WIDE>(B, ((KT) + 3) * BK, lane, w);                     \
+      _Pragma("unroll") for (int jj = 0; jj < 4; ++jj) dma_load_grp(cb, (BP) + OP_BYTES, w, jj);  \
+    }                                                                                             \
+    __builtin_amdgcn_sched_barrier(0);                                                            \
+    pp_sync<8>(rg);                                  /* stage KT + 1 landed */                    \
+    __builtin_amdgcn_sched_barrier(0);                                                            \
+    GG_PP_MFMA()                                     /* step 2 KT + 1: compute stage KT */        \
+    __builtin_amdgcn_sched_barrier(0);                                                            \
+    pp_sync<kNoVm>(rg);                                                                           \
+  }
+    for (int kt = 0; kt < nk; kt += 4) {
+      GG_PP_STAGE1(s0, s3, kt)
+      if (kt + 1 < nk) GG_PP_STAGE1(s1, s0, kt + 1)
+      if (kt + 2 < nk) GG_PP_STAGE1(s2, s1, kt + 2)
+      if (kt + 3 < nk) GG_PP_STAGE1(s3, s2, kt + 3)
     }
 #undef GG_PP_STAGE1
   }
@@ -1454,6 +1669,18 @@ __device__ void decode_groups(const Params& p, int32_t* s_end, int32_t* s_pref, 
     }
     __syncthreads();
   }
+  if constexpr (is_x8(MODE)) {
+    // s_half[g]: the packed scale tiles (256 rows) of the experts before g
+    int64_t local = 0;
+    for (int g = g0; g < g1; ++g) local += (s_end[g] - group_start<MODE>(s_end, g) + BM - 1) / BM;
+    const int64_t incl = block_scan_incl<false, int64_t>(local, scratch, tid);
+    int tiles = (int)(incl - local);
+    for (int g = g0; g < g1; ++g) {
+      s_half[g] = tiles;
+      tiles += (s_end[g] - group_start<MODE>(s_end, g) + BM - 1) / BM;
+    }
+    __syncthreads();
+  }
 }
 
 // Largest g in [0, E) with pref[g] <= t (pref is a non-decreasing
@@ -1517,7 +1744,8 @@ struct Tile {
   uint8_t* cbase;       // output element (first row, first column) of the tile
   uint32_t ldc_bytes;   // output row pitch
   int rows, cols;       // valid output rows / columns of the tile
-  const uint8_t* sa;    // fp8: the tile's packed X scales (k-block 0)
+  const uint8_t* sa;    // fp8: the tile's packed X scales (k-block 0; fp8 wgrad: its first column's)
+  uint32_t sa_left;     // fp8 wgrad: bytes from there to the end of a packed tile
   const uint8_t* sb;    // fp8: the tile's packed W scales
   const uint16_t* bias;   // the expert's bias at the tile's first column, or null
   const float* bscale;    // the bias factor of the tile's first row, or null
@@ -1628,12 +1856,20 @@ __global__ __launch_bounds__(NT, 1) void grouped_gemm_kernel(Params p) {
       const int s = uniform(group_start<MODE>(s_end, g)), e = uniform(s_end[g]);
       // first memory row of the expert's rows (masked: expert g's block)
       const int64_t srow = (is_masked(MODE) ? (int64_t)g * p.m : 0) + s;
-      // A(row kk, red i) = X[srow + i, row0 + kk]
-      A.origin = pa + 2 * (srow * p.k + row0);
-      A.ld_bytes = (uint32_t)(2 * p.k);
+      // A(row kk, red i) = X[srow + i, row0 + kk] (fp8 wgrad: one byte per value)
+      constexpr int asz = is_x8(MODE) ? 1 : 2;
+      A.origin = pa + asz * (srow * p.k + row0);
+      A.ld_bytes = (uint32_t)(asz * p.k);
       A.rows = (int)(p.k - row0 < BM ? p.k - row0 : BM);
       A.red = e - s;
-      A.row_tail = (uint32_t)(2 * (p.k - row0));
+      A.row_tail = (uint32_t)(asz * (p.k - row0));
+      if constexpr (is_x8(MODE)) {
+        // packed scales of the expert's first 256 rows, from the k-block of
+        // the tile's first column on
+        const int64_t xtile = is_masked(MODE) ? (int64_t)g * ((p.m + BM - 1) / BM) : (int64_t)uniform(s_half[g]);
+        T.sa = p.sa + (xtile * (p.k / 128) + row0 / 128) * 256;
+        T.sa_left = (uint32_t)((p.k - row0) / 128 * 256);
+      }
       // B(row n, red i) = dY[srow + i, col0 + n]
       B.origin = pb + 2 * (srow * p.n + col0);
       B.ld_bytes = (uint32_t)(2 * p.n);
@@ -1723,9 +1959,13 @@ __global__ __launch_bounds__(NT, 1) void grouped_gemm_kernel(Params p) {
       }
     }
   };
+  X8Regs x8;            // fp8 wgrad: A on its way to LDS
   auto issue_prologue = [&](const Tile& T) __attribute__((always_inline)) {
     if (T.A.red > 0) {
-      if constexpr (is_fp8(MODE))
+      if constexpr (is_x8(MODE))
+        prologue_loads_x8<WIDE>(sa0, sa1, sa2, T.A.origin, T.B.origin, T.sa, p.k / 128 * 256, T.sa_left, T.A, T.B,
+                                tid, wave, x8);
+      else if constexpr (is_fp8(MODE))
         prologue_loads8_pp(sa0, sa1, sa2, sa0 + OP_BYTES, sa1 + OP_BYTES, sa2 + OP_BYTES, s_sc, T.A.origin,
                            T.B.origin, T.sa, T.sb, (uint32_t)(p.k / 128 * 256), T.A, T.B, tid, wave);
       else if constexpr (PP_PAIR)
@@ -1763,7 +2003,10 @@ __global__ __launch_bounds__(NT, 1) void grouped_gemm_kernel(Params p) {
     const bool half = !is_wgrad(MODE) && cur.rows <= BM / 2;
     // fp32 tiles after the first start with the previous tile's stores
     // still in flight behind their prologue loads
-    if constexpr (is_fp8(MODE)) {
+    if constexpr (is_x8(MODE)) {
+      mainloop_x8<WIDE>(sa0, sa1, sa2, sa3, cur.A.origin, cur.B.origin, cur.sa, p.k / 128 * 256, cur.sa_left, cur.A,
+                        cur.B, tid, wave, faa, fab, acc, prev_stores, x8);
+    } else if constexpr (is_fp8(MODE)) {
       const uint32_t sc_bytes = (uint32_t)(p.k / 128 * 256);
       if (half)
         mainloop8_pp<2>(sa0, sa1, sa2, sa3, sa0 + OP_BYTES, sa1 + OP_BYTES, sa2 + OP_BYTES, sa3 + OP_BYTES,
@@ -1966,6 +2209,29 @@ hipError_t launch_fp8(bool masked, const void* x, const void* sx, const void* w,
   const int grid = (int)(tiles < num_cus ? tiles : num_cus);
   return masked ? launch_mode<FP8_MASKED>(p, out_f32, grid, stream)
                 : launch_mode<FP8>(p, out_f32, grid, stream);
+}
+
+hipError_t launch_fp8_wgrad(bool masked, const void* x, const void* sx, const void* dy, const int32_t* groups,
+                            void* dw, bool out_f32, int64_t m, int64_t k, int64_t n, int32_t num_groups, float alpha,
+                            float beta, int num_cus, hipStream_t stream) {
+  Params p = {};
+  p.a = static_cast<const uint16_t*>(x);
+  p.b = static_cast<const uint16_t*>(dy);
+  p.groups = groups;
+  p.c = dw;
+  p.m = m;
+  p.k = k;
+  p.n = n;
+  p.num_groups = num_groups;
+  p.alpha = alpha;
+  p.beta = beta;
+  p.sa = static_cast<const uint8_t*>(sx);
+  const int64_t tiles = max_tiles(FP8_WGRAD, m, k, n, num_groups);
+  const int grid = (int)(tiles < num_cus ? tiles : num_cus);
+  // the bf16 wgrad's choice of epilogue
+  const bool staged = out_f32 && alpha == 1.0f && beta == 0.0f && (masked ? m : m / num_groups) < kStagedF32Rows;
+  return masked ? launch_wgrad<FP8_MASKED_WGRAD>(p, out_f32, staged, grid, stream)
+                : launch_wgrad<FP8_WGRAD>(p, out_f32, staged, grid, stream);
 }
 
 }  // namespace gg

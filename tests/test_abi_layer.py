@@ -20,7 +20,7 @@ def run(name, defaults, case):
 
 
 POINTERS = {"x", "res", "gamma", "h", "y", "y8", "s8", "dy", "dh", "dx", "dg", "ws", "src", "ss", "rs", "offs", "dst",
-            "ds", "dout", "sr", "w", "dw", "a", "a8", "as8", "h8", "hs8", "da", "act"}
+            "ds", "dout", "sr", "w", "dw", "xs", "a", "a8", "as8", "h8", "hs8", "da", "act"}
 
 NORM = dict(x=A, res=0, gamma=A, h=0, y=A, y8=0, s8=0, rows=4, n=64, eps=1e-6, s=None)
 NORM_GRAD = dict(dy=A, h=A, gamma=A, dh=0, dx=A, dg=A, ws=A, rows=4, n=64, eps=1e-6, s=None)
@@ -157,5 +157,33 @@ I = torch.zeros(4, dtype=torch.int32)
     (ValueError, lambda: gg.silu_mul_grad(bf(4, 8), bf(4, 16), I)),
 ])
 def test_binding_refuses(error, call):
+    with pytest.raises(error):
+        call()
+
+
+WGRAD = dict(x=A, xs=A, dy=A, offs=A, dw=A, dt=1, m=64, k=256, n=64, e=4, alpha=1.0, beta=0.0, s=None)
+
+
+@pytest.mark.parametrize("name", ["gg_fp8_wgrad", "gg_fp8_masked_wgrad"])
+@pytest.mark.parametrize("case,status", [
+    (dict(x=0), 1), (dict(xs=0), 1), (dict(dy=0), 1), (dict(offs=0), 1), (dict(dw=0), 1),
+    (dict(k=64), 2), (dict(k=200), 2), (dict(n=20), 2), (dict(m=-1), 2), (dict(m=BIG), 2),
+    (dict(x=A + 8), 3), (dict(xs=A + 8), 3), (dict(dw=A + 4), 3), (dict(dt=2), 4), (dict(e=0), 5), (dict(e=2049), 5),
+])
+def test_fp8_wgrad_checks_arguments(lib, name, case, status):
+    assert run(name, WGRAD, case) == status, (name, case, gg.last_error())
+
+
+@pytest.mark.parametrize("error,call", [
+    (TypeError, lambda: gg.fp8_wgrad(bf(4, 128), u8(4096), bf(4, 8), I)),
+    (ValueError, lambda: gg.fp8_wgrad(u8(4, 64), u8(4096), bf(4, 8), I)),
+    (ValueError, lambda: gg.fp8_wgrad(u8(4, 128), u8(8), bf(4, 8), I)),
+    (ValueError, lambda: gg.fp8_wgrad(u8(4, 128), u8(4096), bf(5, 8), I)),
+    (ValueError, lambda: gg.fp8_wgrad(u8(4, 128), u8(4096), bf(4, 8), I, beta=1.0)),
+    (ValueError, lambda: gg.fp8_wgrad(u8(4, 128), u8(4096), bf(4, 8), I, out=torch.zeros(4, 8, 128))),
+    (TypeError, lambda: gg.fp8_wgrad(u8(4, 128), u8(4096), bf(4, 8), I, out=torch.zeros(4, 128, 8).half())),
+    (ValueError, lambda: gg.fp8_masked_wgrad(u8(3, 4, 128), u8(4096), bf(3, 4, 8), I)),
+])
+def test_fp8_wgrad_binding_refuses(error, call):
     with pytest.raises(error):
         call()
