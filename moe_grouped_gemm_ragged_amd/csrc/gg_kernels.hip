@@ -706,20 +706,32 @@ __device__ __attribute__((always_inline)) inline void mainloop_x8(
     __builtin_amdgcn_sched_barrier(0);                                                            \
     pp_sync<kNoVm>(rg);                              /* fragments in registers, A written */      \
   }
-    for (int kt = 0; kt < nk; kt += 4) {
+    // Whole rounds of four stages, then the rest: a stage that may be skipped
+    // inside the loop would make the compiler wait, on every path, for loads
+    // that are still wanted in flight.
+    int kt = 0;
+    for (; kt + 4 <= nk; kt += 4) {
       x8_scales(sa, tile_bytes, sc_left, (kt + 4) * BK, A.red, lane, w, next);
       GG_PP_STAGE0(s1, s2, x.even, x.sc, 2, kt)
-      // (leaving the loop, rather than skipping a stage and going on: a path
-      // on which the next stage comes without the loads of this one would make
-      // the compiler wait for loads that are still wanted in flight)
-      if (kt + 1 >= nk) break;
       GG_PP_STAGE0(s2, s3, x.odd, x.sc, 3, kt + 1)
-      if (kt + 2 >= nk) break;
       GG_PP_STAGE0(s3, s0, x.even, next, 0, kt + 2)
-      if (kt + 3 >= nk) break;
       GG_PP_STAGE0(s0, s1, x.odd, next, 1, kt + 3)
       x.sc[0] = next[0];
       x.sc[1] = next[1];
+    }
+    if (kt < nk) {
+      GG_PP_STAGE0(s1, s2, x.even, x.sc, 2, kt)
+      if (kt + 1 < nk) {
+        GG_PP_STAGE0(s2, s3, x.odd, x.sc, 3, kt + 1)
+        if (kt + 2 < nk) {
+          // nothing is left to read or to write
+          __builtin_amdgcn_sched_barrier(0);
+          GG_PP_MFMA()
+          __builtin_amdgcn_sched_barrier(0);
+          pp_sync<kNoVm>(rg);
+          pp_sync<kNoVm>(rg);
+        }
+      }
     }
 #undef GG_PP_STAGE0
   } else {
