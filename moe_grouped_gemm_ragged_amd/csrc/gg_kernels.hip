@@ -2216,13 +2216,14 @@ static hipError_t launch_mode(const Params& p, bool out_f32, int grid, hipStream
 template <int MODE>
 static hipError_t launch_wgrad(const Params& p, bool out_f32, bool staged, int grid, hipStream_t stream) {
   const int64_t widest = 2 * (p.k > p.n ? p.k : p.n);
-  if (p.m * widest < (int64_t(1) << 32)) {
-    if (staged) return launch_one<MODE, true, true>(p, grid, stream);
-    return launch_mode<MODE>(p, out_f32, grid, stream);
-  }
-  if (staged) return launch_one<MODE, true, true, true>(p, grid, stream);
-  return out_f32 ? launch_one<MODE, true, false, true>(p, grid, stream)
-                 : launch_one<MODE, false, false, true>(p, grid, stream);
+  const bool narrow = p.m * widest < (int64_t(1) << 32);
+  if (staged)
+    return narrow ? launch_one<MODE, true, true>(p, grid, stream)
+                  : launch_one<MODE, true, true, true>(p, grid, stream);
+  if constexpr (!is_x8(MODE))     // (fp32 is always staged there)
+    if (out_f32)
+      return narrow ? launch_one<MODE, true>(p, grid, stream) : launch_one<MODE, true, false, true>(p, grid, stream);
+  return narrow ? launch_one<MODE, false>(p, grid, stream) : launch_one<MODE, false, false, true>(p, grid, stream);
 }
 
 // Upper bound on the number of output tiles, from host-known sizes only
@@ -2324,10 +2325,11 @@ hipError_t launch_fp8_wgrad(bool masked, const void* x, const void* sx, const vo
   p.sa = static_cast<const uint8_t*>(sx);
   const int64_t tiles = max_tiles(FP8_WGRAD, m, k, n, num_groups);
   const int grid = (int)(tiles < num_cus ? tiles : num_cus);
-  // the bf16 wgrad's choice of epilogue
-  const bool staged = out_f32 && alpha == 1.0f && beta == 0.0f && (masked ? m : m / num_groups) < kStagedF32Rows;
-  return masked ? launch_wgrad<FP8_MASKED_WGRAD>(p, out_f32, staged, grid, stream)
-                : launch_wgrad<FP8_WGRAD>(p, out_f32, staged, grid, stream);
+  // fp32 always through LDS: its whole rows beat stores straight from the
+  // accumulators here for long experts too (16 experts of 4096 rows, k 4096,
+  // n 2048: 970 against 978 us)
+  return masked ? launch_wgrad<FP8_MASKED_WGRAD>(p, out_f32, out_f32, grid, stream)
+                : launch_wgrad<FP8_WGRAD>(p, out_f32, out_f32, grid, stream);
 }
 
 }  // namespace gg
