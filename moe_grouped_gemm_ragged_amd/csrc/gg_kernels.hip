@@ -92,6 +92,7 @@ constexpr int STAGE_BYTES = 2 * OP_BYTES;   // A then B: 32 KB
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float floatx16 __attribute__((ext_vector_type(16)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef short shortx4 __attribute__((ext_vector_type(4)));
 
 #define LDS_PTR(p) ((__attribute__((address_space(3))) void*)(p))
@@ -551,38 +552,39 @@ __device__ __attribute__((always_inline)) inline void mainloop_pp(
 // reduction); instead X becomes bf16 on its way into LDS -- exactly: an e4m3
 // value has 4 significant bits and the scale only moves its exponent -- and
 // fragments and MFMAs are those of the bf16 wgrad.  So group 0 moves A through
-// registers: two 16-byte loads per lane and stage (half the bytes of bf16),
-// converted 16 columns at a time (one scale each) and written to LDS in the
+// registers: four 8-byte loads per lane and stage (half the bytes of bf16),
+// converted 8 columns at a time (one scale each) and written to LDS in the
 // red-strided layout.  Its step 2s + 1 reads the fragments of stage s + 1,
 // converts and writes A of stage s + 2 and loads A of stage s + 4 into the
 // registers that frees: 4 steps from load to use, and the write is two
 // barriers ahead of its first reader.  Group 1 is the bf16 schedule's.
 
 // A of two stages on its way, and the scales of their 128 reduction rows: a
-// dword for each of this lane's two rows of a stage (16 jj + lane / 4), byte
+// dword for each of this lane's four rows of a stage (8 jj + lane / 8), byte
 // s mod 4 for stage s.
 struct X8Regs {
-  u32x4 even[2], odd[2];
-  uint32_t sc[2];
+  u32x2 even[4], odd[4];
+  uint32_t sc[4];
 };
 
-// Load jj of wave w covers reduction rows 16 jj .. + 15 of tile columns 64 w
-// .. + 63: lane i row 16 jj + i / 4, columns 16 (i mod 4) .. + 15.  Rows past
-// the expert's last one read as zero; columns past k belong to tile rows that
-// are not stored.
+// Load jj of wave w covers reduction rows 8 jj .. + 7 of tile columns 64 w
+// .. + 63: lane i row 8 jj + i / 8, columns 8 (i mod 8) .. + 7.  (8 bytes a
+// lane, not 16: a lane's values are then one 16-byte chunk of bf16, and the
+// lanes' chunks are consecutive in LDS.)  Rows past the expert's last one read
+// as zero; columns past k belong to tile rows that are not stored.
 template <bool WIDE>
-__device__ __forceinline__ void x8_load(const Operand& op, int q0, int lane_in, int w, u32x4 (&r)[2]) {
+__device__ __forceinline__ void x8_load(const Operand& op, int q0, int lane_in, int w, u32x2 (&r)[4]) {
   const int lane = (int)opaque_v((uint32_t)lane_in);
   const int left = op.red - q0;
   int last = left - 1;
   if constexpr (WIDE) last = last < 63 ? last : 63;
   const uint32_t nrec = left > 0 ? (uint32_t)last * op.ld_bytes + op.row_tail : 0u;
   const __amdgpu_buffer_rsrc_t rs = make_rsrc(op.origin + (int64_t)q0 * op.ld_bytes, nrec);
-  const uint32_t voff = (uint32_t)(lane >> 2) * op.ld_bytes + (uint32_t)(64 * w + 16 * (lane & 3));
+  const uint32_t voff = (uint32_t)(lane >> 3) * op.ld_bytes + (uint32_t)(64 * w + 8 * (lane & 7));
 #pragma unroll
-  for (int jj = 0; jj < 2; ++jj)
-    r[jj] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                                          rs, voff + (uint32_t)(16 * jj) * op.ld_bytes, 0, 0));
+  for (int jj = 0; jj < 4; ++jj)
+    r[jj] = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(
+                                          rs, voff + (uint32_t)(8 * jj) * op.ld_bytes, 0, 0));
 }
 
 // Scale dwords of reduction rows q0 .. q0 + 127 (q0 a multiple of 128): sa
@@ -590,37 +592,31 @@ __device__ __forceinline__ void x8_load(const Operand& op, int q0, int lane_in, 
 // tile's first column on; tile_bytes a packed tile's bytes, left those from
 // that k-block to its end (a tile's last columns may have no k-block).
 __device__ __forceinline__ void x8_scales(const uint8_t* sa, int64_t tile_bytes, uint32_t left, int q0, int red,
-                                          int lane_in, int w, uint32_t (&sc)[2]) {
+                                          int lane_in, int w, uint32_t (&sc)[4]) {
   const int lane = (int)opaque_v((uint32_t)lane_in);
   const __amdgpu_buffer_rsrc_t rs = make_rsrc(sa + (int64_t)(q0 >> 8) * tile_bytes, q0 < red ? left : 0u);
-  const uint32_t voff = (uint32_t)(256 * (w >> 1) + ((q0 >> 7) & 1) * 128 + 4 * (lane >> 2));
+  const uint32_t voff = (uint32_t)(256 * (w >> 1) + ((q0 >> 7) & 1) * 128 + 4 * (lane >> 3));
 #pragma unroll
-  for (int jj = 0; jj < 2; ++jj) sc[jj] = __builtin_amdgcn_raw_buffer_load_b32(rs, voff + 64 * jj, 0, 0);
+  for (int jj = 0; jj < 4; ++jj) sc[jj] = __builtin_amdgcn_raw_buffer_load_b32(rs, voff + 32 * jj, 0, 0);
 }
 
 // Converts a stage and writes it to its A region; byte: the stage's byte of
 // the scale dwords.
-__device__ __forceinline__ void x8_write(const u32x4 (&r)[2], const uint32_t (&sc)[2], int byte, int lane_in, int w,
+__device__ __forceinline__ void x8_write(const u32x2 (&r)[4], const uint32_t (&sc)[4], int byte, int lane_in, int w,
                                          uint8_t* lds_op) {
-  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
   const int lane = (int)opaque_v((uint32_t)lane_in);
+  const int chunk = (lane & 7) ^ (4 * ((lane >> 4) & 1));
+  uint8_t* to = lds_op + 4096 * w + 128 * (lane >> 3) + 16 * chunk;
 #pragma unroll
-  for (int jj = 0; jj < 2; ++jj) {
+  for (int jj = 0; jj < 4; ++jj) {
     const float scale = __builtin_bit_cast(float, ((sc[jj] >> (8 * byte)) & 0xFFu) << 23);
-    const int q = 16 * jj + (lane >> 2);
+    u32x4 o;
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      u32x4 o;
-#pragma unroll
-      for (int d = 0; d < 2; ++d) {
-        const bf16x2 lo = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(r[jj][2 * e + d], scale, false);
-        const bf16x2 hi = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(r[jj][2 * e + d], scale, true);
-        o[2 * d] = __builtin_bit_cast(uint32_t, lo);
-        o[2 * d + 1] = __builtin_bit_cast(uint32_t, hi);
-      }
-      const int chunk = (2 * (lane & 3) + e) ^ (4 * ((q >> 1) & 1));
-      *reinterpret_cast<u32x4*>(lds_op + 4096 * w + 128 * q + 16 * chunk) = o;
+    for (int d = 0; d < 2; ++d) {
+      o[2 * d] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(r[jj][d], scale, false));
+      o[2 * d + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(r[jj][d], scale, true));
     }
+    *reinterpret_cast<u32x4*>(to + 1024 * jj) = o;
   }
 }
 
@@ -684,7 +680,7 @@ __device__ __attribute__((always_inline)) inline void mainloop_x8(
     read_stage_frags<true, true, TM>(BUF, (BUF) + OP_BYTES, faa, fab, 1, f1);                     \
   }
   if (g0) {
-    uint32_t next[2];
+    uint32_t next[4];
     x8_write(x.even, x.sc, 0, lane, w, s0);
     x8_load<WIDE>(A, 2 * BK, lane, w, x.even);
     x8_write(x.odd, x.sc, 1, lane, w, s1);
@@ -716,8 +712,8 @@ __device__ __attribute__((always_inline)) inline void mainloop_x8(
       GG_PP_STAGE0(s2, s3, x.odd, x.sc, 3, kt + 1)
       GG_PP_STAGE0(s3, s0, x.even, next, 0, kt + 2)
       GG_PP_STAGE0(s0, s1, x.odd, next, 1, kt + 3)
-      x.sc[0] = next[0];
-      x.sc[1] = next[1];
+#pragma unroll
+      for (int jj = 0; jj < 4; ++jj) x.sc[jj] = next[jj];
     }
     if (kt < nk) {
       GG_PP_STAGE0(s1, s2, x.even, x.sc, 2, kt)
