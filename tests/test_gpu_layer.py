@@ -177,6 +177,33 @@ def test_fp8_gather_rows_bit_exact(seed, tokens, topk, e, align, pad, drop, k):
     assert torch.equal(packed.cpu(), ref.packed_scales(rows, offs.tolist(), cap, fill=0xA5))
 
 
+@pytest.mark.parametrize("tokens,topk,e,k,align,pad,drop", [
+    (4100, 2, 3, 2176, 8, True, 0.0), (9000, 3, 40, 1024, 1, False, 0.05), (20000, 2, 300, 512, 4, True, 0.0),
+    (1300, 6, 2048, 7168, 1, False, 0.0), (1100, 4, 16, 8320, 16, True, 0.02), (70000, 2, 5, 128, 8, True, 0.0)])
+def test_fp8_gather_rows_of_many_tokens(tokens, topk, e, k, align, pad, drop):
+    """More than 8 MB of tokens, which are copied window by window."""
+    dev = device()
+    assert tokens * k > 8 << 20
+    g = gen(tokens)
+    offs, row_slot, _ = routing(tokens, tokens, topk, e, align, pad, drop)
+    cap, used = row_slot.shape[0], int(offs[-1])
+    src = torch.randint(0, 256, (tokens, k), generator=g, device=dev, dtype=U8)
+    scales = torch.randint(1, 255, (tokens, k // 128), generator=g, device=dev, dtype=U8)
+    out = torch.full((cap, k), 0xA5, dtype=U8, device=dev)
+    say("fp8_gather_rows of many tokens", tokens, topk, e, k)
+    _, packed = gg.fp8_gather_rows(src, scales, row_slot, topk, offs, out=out)
+    slot = row_slot[:used].long()
+    want = torch.where((slot >= 0)[:, None], src[slot.clamp(min=0) // topk], torch.zeros(1, dtype=U8, device=dev))
+    assert torch.equal(out[:used], want)
+    assert bool((out[used:] == 0xA5).all()), "rows past the last offset were written"
+    raw = torch.where((slot >= 0)[:, None], scales[slot.clamp(min=0) // topk],
+                      torch.full((1, 1), 127, dtype=U8, device=dev))
+    same = gg.fp8_pack_scales(gg.GG_FP8_ACT_RAGGED, raw.contiguous(), offs, used, k, e)
+    tiles = int(((torch.diff(offs.long(), prepend=offs.new_zeros(1).long()) + 255) // 256).sum())
+    n = tiles * (k // 128) * 256
+    assert torch.equal(packed[:n], same[:n])
+
+
 def test_fp8_gather_rows_feeds_the_packed_layout():
     """The scales are those that gg_fp8_pack_scales writes for the gathered rows."""
     dev = device()
@@ -187,10 +214,11 @@ def test_fp8_gather_rows_feeds_the_packed_layout():
     say("fp8_gather_rows against pack_scales")
     rows, packed = gg.fp8_gather_rows(src, scales, row_slot, 4, offs, out_scales=torch.zeros(
         gg.fp8_scale_bytes(gg.GG_FP8_ACT_RAGGED, row_slot.shape[0], k, 12), dtype=U8, device=dev))
-    slot = row_slot.long()
-    raw = torch.where((slot >= 0)[:, None], scales[slot.clamp(min=0) // 4], torch.full((1, k // 128), 127, dtype=U8, device=dev))
-    raw[used:] = 0
-    want = gg.fp8_pack_scales(gg.GG_FP8_ACT_RAGGED, raw.contiguous(), offs, row_slot.shape[0], k, 12,
+    slot = row_slot[:used].long()                         # (what lies behind them is not initialised)
+    raw = torch.zeros(row_slot.shape[0], k // 128, dtype=U8, device=dev)
+    raw[:used] = torch.where((slot >= 0)[:, None], scales[slot.clamp(min=0) // 4],
+                             torch.full((1, 1), 127, dtype=U8, device=dev))
+    want = gg.fp8_pack_scales(gg.GG_FP8_ACT_RAGGED, raw, offs, row_slot.shape[0], k, 12,
                               out=torch.zeros_like(packed))
     assert torch.equal(packed, want)
 
