@@ -804,13 +804,22 @@ def _launch(name, dev, *args):
     torch = _torch()
     if dev.type != "cuda":
         raise ValueError(f"{name}: the tensors are on {dev}, expected a GPU")
+    f = getattr(load(), name)
     if torch.cuda.current_device() == dev.index:
-        rc = call_raw(name, *args, _stream_handle(dev))
+        rc = f(*args, _raw_stream(dev.index))
     else:
         with torch.cuda.device(dev):
-            rc = call_raw(name, *args, _stream_handle(dev))
+            rc = f(*args, _raw_stream(dev.index))
     if rc != 0:
         raise GGError(name, rc, last_error())
+
+
+def _raw_stream(index):
+    """The current stream's handle without a Stream object around it (2 us of
+    a small call's 10), where this torch has that."""
+    torch = _torch()
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return raw(index) if raw is not None else int(torch.cuda.current_stream(index).cuda_stream)
 
 
 def _shaped(t, name, dtype, shape, device):
@@ -818,7 +827,7 @@ def _shaped(t, name, dtype, shape, device):
     if t is None:
         return _torch().empty(shape, dtype=dtype, device=device)
     _check(t, name, dtype, len(shape), device)
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
     return t
 

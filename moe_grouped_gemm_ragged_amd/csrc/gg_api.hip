@@ -653,7 +653,7 @@ gg_status gg_rmsnorm(const void* x, const void* residual, const void* gamma, voi
 
 int64_t gg_rmsnorm_grad_workspace_bytes(int64_t rows, int64_t n) {
   if (rows < 0 || rows >= kRowLimit || n < 8 || n % 8 != 0 || n > GG_MAX_KN) return -1;
-  const int64_t g = gg::rmsnorm_grad_groups(rows);
+  const int64_t g = gg::rmsnorm_grad_groups(rows, n);
   return (g > 0 ? g : 1) * n * 4;
 }
 

@@ -102,7 +102,8 @@ constexpr int kUnits = 8;       // 1 KB pieces a wave moves at a time
 
 // Copies kUnits / CH rows (CH pieces of 1 KB each; CH = 8: any longer row, 8
 // KB after 8 KB), all loads before the first store.  Lane i < R brings row i
-// and its slot (row < 0: none).  NT: stores that leave the caches to src.
+// and its slot (row < 0: none).  NT: stores that leave the caches to src (not
+// for few rows, which the GEMM then finds in the caches).
 template <int CH, bool NT>
 __device__ __forceinline__ void copy_rows(const uint8_t* src, int64_t row, int32_t slot, int32_t topk, int64_t tokens,
                                           int64_t k, uint8_t* dst) {
@@ -132,8 +133,8 @@ __device__ __forceinline__ void copy_rows(const uint8_t* src, int64_t row, int32
     for (int u = 0; u < kUnits; ++u) {
       const int64_t c = c0 + 1024 * (u % CH);
       if (live[u / CH] && c < k) {
-        if constexpr (NT) __builtin_nontemporal_store(v[u], reinterpret_cast<u32x4r*>(to[u / CH] + c));
-        else store16(to[u / CH] + c, v[u]);
+        if constexpr (NT) store16(to[u / CH] + c, v[u]);
+        else *reinterpret_cast<u32x4r*>(to[u / CH] + c) = v[u];
       }
     }
   }

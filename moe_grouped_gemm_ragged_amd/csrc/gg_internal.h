@@ -96,9 +96,9 @@ hipError_t launch_dscale(bool masked, const void* dy, const int32_t* groups, con
                          int64_t n, int32_t E, float* ds, int num_cus, hipStream_t stream);
 
 // Norm with the residual's addition and its gradient (gg_norm.hip).  Null:
-// res, h, y, y8 with scales; dh.  part holds rmsnorm_grad_groups(rows) rows of
+// res, h, y, y8 with scales; dh.  part holds rmsnorm_grad_groups(rows, n) rows of
 // n floats.
-int64_t rmsnorm_grad_groups(int64_t rows);
+int64_t rmsnorm_grad_groups(int64_t rows, int64_t n);
 hipError_t launch_rmsnorm(const void* x, const void* res, const void* gamma, void* h, void* y, void* y8,
                           void* scales, int64_t rows, int64_t n, float eps, hipStream_t stream);
 hipError_t launch_rmsnorm_grad(const void* dy, const void* h, const void* gamma, const void* dh, void* dx,

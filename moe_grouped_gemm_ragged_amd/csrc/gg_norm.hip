@@ -34,7 +34,8 @@ constexpr int kMaxWaves = kMaxThreads / 64;
 // Sums over the T threads of a row (waves = T / 64; one wave needs no
 // barrier).  red holds two buffers used in turn: a row's writes touch the one
 // that the previous row did not read, and the row after it comes behind the
-// next row's barrier.
+// next row's barrier.  A workgroup of several rows (blockDim.y) calls it
+// together.
 template <int N>
 struct RowSums {
   float (*red)[N * kMaxWaves];
@@ -43,7 +44,8 @@ struct RowSums {
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] = wave_sum(v[i]);
     if (waves == 1) return;
-    float* r = red[turn];
+    const int first = waves * threadIdx.y;
+    float* r = red[turn] + first;
     turn ^= 1;
     if ((threadIdx.x & 63) == 0)
 #pragma unroll
@@ -87,7 +89,7 @@ __device__ __forceinline__ void store_norm(const NormOut& out, const uint16_t* g
   if (out.y) store16(out.y + at, pack8(v));
   if (out.y8) {
     int byte;
-    *reinterpret_cast<u32x2r*>(out.y8 + at) = quantise8(v, byte);
+    store8(out.y8 + at, quantise8(v, byte));
     if ((c & 15) == 0) out.scales[row * (n / kBlock) + c / 16] = (uint8_t)byte;
   }
 }
@@ -152,18 +154,21 @@ __global__ __launch_bounds__(kMaxThreads) void rmsnorm_long_kernel(const uint16_
 
 // ---- gradient ------------------------------------------------------------------------
 
-// Workgroup b takes rows b, b + G, ... and keeps its share of dgamma in
-// registers, written at the end to row b of the workspace: no atomics, so the
-// sum's order is fixed.
+// A workgroup takes blockDim.y = Y rows at a time, T = blockDim.x threads
+// each: workgroup b rows Y b .., Y (b + G) .., and so on.  Each slice keeps
+// its share of dgamma in registers; at the end the slices are added in order
+// and written to row b of the workspace: no atomics, so the sum's order is
+// fixed.
 template <int VPT>
 __global__ __launch_bounds__(kMaxThreads) void rmsnorm_grad_kernel(const uint16_t* dy, const uint16_t* h,
                                                                    const uint16_t* gamma, const uint16_t* dh,
                                                                    uint16_t* dx, float* part, int64_t rows,
                                                                    int64_t n, float eps) {
   __shared__ float red[2][2 * kMaxWaves];
+  __shared__ f32x4r slices[kMaxThreads * 2];
   RowSums<2> sums = {red, 0};
-  const int T = blockDim.x;
-  const int t = threadIdx.x;
+  const int T = blockDim.x, Y = blockDim.y;
+  const int t = threadIdx.x, y = threadIdx.y;
   const int waves = T / 64;
   const int groups = (int)(n / 8);
   const float rn = 1.0f / (float)n;
@@ -177,14 +182,17 @@ __global__ __launch_bounds__(kMaxThreads) void rmsnorm_grad_kernel(const uint16_
 #pragma unroll
     for (int e = 0; e < 8; ++e) dg[j][e] = 0.f;
   }
-  for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
+  // every slice goes through the loop equally often (the sums' barriers)
+  for (int64_t first = (int64_t)blockIdx.x * Y; first < rows; first += (int64_t)gridDim.x * Y) {
+    const int64_t row = first + y;
+    const bool live = row < rows;
     u32x4r hq[VPT], dq[VPT], rq[VPT];
     float s[2] = {0.f, 0.f};
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
       const int c = t + j * T;
       hq[j] = dq[j] = rq[j] = u32x4r{0u, 0u, 0u, 0u};
-      if (c < groups) {
+      if (live && c < groups) {
         hq[j] = load16(h + row * n + 8 * c);
         dq[j] = load16(dy + row * n + 8 * c);
         if (dh) rq[j] = load16(dh + row * n + 8 * c);
@@ -203,6 +211,7 @@ __global__ __launch_bounds__(kMaxThreads) void rmsnorm_grad_kernel(const uint16_
       }
     }
     sums(s, waves);
+    if (!live) continue;             // (eps may be 0: no 0 / 0 into the sums)
     const float rho = 1.0f / sqrtf(s[0] * rn + eps);
     const float m = s[1] * rn * rho;        // mean of p (h rho)
 #pragma unroll
@@ -225,10 +234,22 @@ __global__ __launch_bounds__(kMaxThreads) void rmsnorm_grad_kernel(const uint16_
 #pragma unroll
   for (int j = 0; j < VPT; ++j) {
     const int c = t + j * T;
-    if (c < groups) {
+    f32x4r lo = {dg[j][0], dg[j][1], dg[j][2], dg[j][3]}, hi = {dg[j][4], dg[j][5], dg[j][6], dg[j][7]};
+    if (Y > 1) {
+      __syncthreads();               // the round before has been read
+      slices[2 * (y * T + t)] = lo;
+      slices[2 * (y * T + t) + 1] = hi;
+      __syncthreads();
+      if (y == 0)
+        for (int z = 1; z < Y; ++z) {
+          lo += slices[2 * (z * T + t)];
+          hi += slices[2 * (z * T + t) + 1];
+        }
+    }
+    if (y == 0 && c < groups) {
       float* p = part + (int64_t)blockIdx.x * n + 8 * c;
-      *reinterpret_cast<f32x4r*>(p) = f32x4r{dg[j][0], dg[j][1], dg[j][2], dg[j][3]};
-      *reinterpret_cast<f32x4r*>(p + 4) = f32x4r{dg[j][4], dg[j][5], dg[j][6], dg[j][7]};
+      *reinterpret_cast<f32x4r*>(p) = lo;
+      *reinterpret_cast<f32x4r*>(p + 4) = hi;
     }
   }
 }
@@ -317,11 +338,24 @@ constexpr int64_t kLongRow = 8 * 4 * kMaxThreads;
 constexpr int64_t kLongGradRow = 8 * 2 * kMaxThreads;
 
 constexpr int64_t kMostBlocks = 1 << 20;   // a launch's threads stay below 2^32
-constexpr int kGradGroups = 512;   // workgroups (workspace rows) of the gradient at most
+
+// Threads of a workgroup of the gradient, in slices of a row each, and the
+// most workgroups (workspace rows): one large workgroup a compute unit keeps
+// the workspace small and still has its waves' loads in flight.  8192 x 6144:
+// 82 us (4.9 TB/s) with 256 workgroups of 768, 86 with 512 of 512 or of a
+// single slice; 16384 x 512: 18.3 us, 34.9 with 512 of a single slice.
+constexpr int kGradThreads = 768;
+constexpr int kGradGroups = 256;
+int grad_slices(int threads) { return threads >= kGradThreads ? 1 : kGradThreads / threads; }
+int grad_groups(int64_t rows, int64_t n) {
+  const int64_t per = n > kLongGradRow ? 1 : grad_slices(shape_of(n / 8).threads);
+  const int64_t want = (rows + per - 1) / per;
+  return (int)(want < kGradGroups ? want : kGradGroups);
+}
 
 }  // namespace
 
-int64_t rmsnorm_grad_groups(int64_t rows) { return rows < kGradGroups ? rows : kGradGroups; }
+int64_t rmsnorm_grad_groups(int64_t rows, int64_t n) { return grad_groups(rows, n); }
 
 hipError_t launch_rmsnorm(const void* x, const void* res, const void* gamma, void* h, void* y, void* y8,
                           void* scales, int64_t rows, int64_t n, float eps, hipStream_t stream) {
@@ -351,18 +385,19 @@ hipError_t launch_rmsnorm_grad(const void* dy, const void* h, const void* gamma,
   const uint16_t* gp = static_cast<const uint16_t*>(gamma);
   const uint16_t* rp = static_cast<const uint16_t*>(dh);
   uint16_t* xp = static_cast<uint16_t*>(dx);
-  const int G = (int)rmsnorm_grad_groups(rows);
+  const int G = grad_groups(rows, n);
   if (G > 0) {
     hipError_t e;
     const Shape s = shape_of(n / 8);
+    const dim3 block(s.threads, grad_slices(s.threads));
     if (n > kLongGradRow)
       e = launch_kernel(rmsnorm_grad_long_kernel, dim3(G), dim3(kMaxThreads), stream, dp, hp, gp, rp, xp, part, rows,
                         n, eps);
     else if (s.vpt == 1)
-      e = launch_kernel(rmsnorm_grad_kernel<1>, dim3(G), dim3(s.threads), stream, dp, hp, gp, rp, xp, part, rows, n,
+      e = launch_kernel(rmsnorm_grad_kernel<1>, dim3(G), block, stream, dp, hp, gp, rp, xp, part, rows, n,
                         eps);
     else
-      e = launch_kernel(rmsnorm_grad_kernel<2>, dim3(G), dim3(s.threads), stream, dp, hp, gp, rp, xp, part, rows, n,
+      e = launch_kernel(rmsnorm_grad_kernel<2>, dim3(G), block, stream, dp, hp, gp, rp, xp, part, rows, n,
                         eps);
     if (e != hipSuccess) return e;
   }

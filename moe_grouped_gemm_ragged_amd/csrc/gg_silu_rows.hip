@@ -95,13 +95,13 @@ __global__ __launch_bounds__(kThreads) void silu_mul_rows_kernel(const uint16_t*
     const bool lead = (w.group & 15) == 0;
     int byte;
     if (out.a8) {
-      *reinterpret_cast<u32x2r*>(out.a8 + to) = quantise8(a, byte);
+      store8(out.a8 + to, quantise8(a, byte));
       if (lead) out.a8_scales[w.row * kb + w.group / 16] = (uint8_t)byte;
     }
     if (out.h8) {
-      *reinterpret_cast<u32x2r*>(out.h8 + at) = quantise8(g, byte);
+      store8(out.h8 + at, quantise8(g, byte));
       if (lead) out.h8_scales[w.row * 2 * kb + w.group / 16] = (uint8_t)byte;
-      *reinterpret_cast<u32x2r*>(out.h8 + at + width) = quantise8(u, byte);
+      store8(out.h8 + at + width, quantise8(u, byte));
       if (lead) out.h8_scales[w.row * 2 * kb + kb + w.group / 16] = (uint8_t)byte;
     }
   }

@@ -53,9 +53,11 @@ def test_rmsnorm_grad_checks_arguments(lib, case, status):
 
 
 def test_rmsnorm_grad_workspace(lib):
-    assert gg.rmsnorm_grad_workspace_bytes(0, 64) == 64 * 4
-    assert gg.rmsnorm_grad_workspace_bytes(3, 64) == 3 * 64 * 4
-    assert gg.rmsnorm_grad_workspace_bytes(1 << 20, 64) >= 64 * 4
+    # a whole number of fp32 rows, one at least, no more than there are rows of h
+    for rows in (0, 1, 3, 1000, 1 << 20):
+        for n in (8, 64, 7168, 1 << 20):
+            size = gg.rmsnorm_grad_workspace_bytes(rows, n)
+            assert size % (4 * n) == 0 and 1 <= size // (4 * n) <= max(1, rows)
     for rows, n in ((-1, 64), (4, 12), (4, 0), (BIG, 64)):
         assert lib.gg_rmsnorm_grad_workspace_bytes(rows, n) == -1
 
