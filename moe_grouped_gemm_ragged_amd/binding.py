@@ -822,10 +822,12 @@ def _raw_stream(index):
     return raw(index) if raw is not None else int(torch.cuda.current_stream(index).cuda_stream)
 
 
-def _shaped(t, name, dtype, shape, device):
-    """``t`` checked against a shape, or a new tensor of it."""
+def _shaped(t, name, dtype, shape, device, like=None):
+    """``t`` checked against a shape, or a new tensor of it (that ``like``
+    has too, where there is one: the cheaper call)."""
     if t is None:
-        return _torch().empty(shape, dtype=dtype, device=device)
+        torch = _torch()
+        return torch.empty(shape, dtype=dtype, device=device) if like is None else torch.empty_like(like)
     _check(t, name, dtype, len(shape), device)
     if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
@@ -839,12 +841,11 @@ def _ptr(t):
 def _rmsnorm(x, gamma, residual, eps, y, y8, scales, h):
     torch = _torch()
     dev = x.device
-    _check(x, "x", torch.bfloat16, 2, dev)
     rows, n = x.shape
     _shaped(gamma, "gamma", torch.bfloat16, (n,), dev)
     if residual is not None:
         _shaped(residual, "residual", torch.bfloat16, (rows, n), dev)
-        h = _shaped(h, "h_out", torch.bfloat16, (rows, n), dev)
+        h = _shaped(h, "h_out", torch.bfloat16, (rows, n), dev, like=x)
     elif h is not None:
         raise ValueError("h_out without a residual: h is x itself")
     _launch("gg_rmsnorm", dev, _ptr(x), _ptr(residual), _ptr(gamma), _ptr(h), _ptr(y), _ptr(y8), _ptr(scales), rows,
@@ -857,7 +858,8 @@ def rmsnorm(x, gamma, residual=None, eps=1e-6, out=None, h_out=None):
     bf16 [n].  Returns (y, h) with h = x + residual in bf16 (``h_out``, which
     may be ``residual`` or ``x``), or h = None without a residual."""
     torch = _torch()
-    y = _shaped(out, "out", torch.bfloat16, tuple(x.shape), x.device)
+    _check(x, "x", torch.bfloat16, 2, x.device)
+    y = _shaped(out, "out", torch.bfloat16, x.shape, x.device, like=x)
     h = _rmsnorm(x, gamma, residual, eps, y, None, None, h_out)
     return y, h
 
@@ -867,13 +869,14 @@ def fp8_rmsnorm(x, gamma, residual=None, eps=1e-6, out=None, out_scales=None, h_
     [rows, n / 128] (n a multiple of 128).  Returns (codes, scales, h), or
     (codes, scales, h, y) with the bf16 y too (``with_bf16``)."""
     torch = _torch()
-    if x.dim() != 2 or x.shape[1] % 128:
-        raise ValueError("x must be [rows, n] with n a multiple of 128")
-    rows, n = x.shape
     dev = x.device
+    _check(x, "x", torch.bfloat16, 2, dev)
+    rows, n = x.shape
+    if n % 128:
+        raise ValueError("x must be [rows, n] with n a multiple of 128")
     y8 = _shaped(out, "out", torch.uint8, (rows, n), dev)
     scales = _shaped(out_scales, "out_scales", torch.uint8, (rows, n // 128), dev)
-    y = torch.empty((rows, n), dtype=torch.bfloat16, device=dev) if with_bf16 else None
+    y = torch.empty_like(x) if with_bf16 else None
     h = _rmsnorm(x, gamma, residual, eps, y, y8, scales, h_out)
     return (y8, scales, h, y) if with_bf16 else (y8, scales, h)
 
@@ -897,7 +900,7 @@ def rmsnorm_grad(dy, h, gamma, dh=None, eps=1e-6, out=None, dgamma=None, workspa
     _shaped(gamma, "gamma", torch.bfloat16, (n,), dev)
     if dh is not None:
         _shaped(dh, "dh", torch.bfloat16, (rows, n), dev)
-    dx = _shaped(out, "out", torch.bfloat16, (rows, n), dev)
+    dx = _shaped(out, "out", torch.bfloat16, (rows, n), dev, like=dy)
     dgamma = _shaped(dgamma, "dgamma", torch.float32, (n,), dev)
     need = rmsnorm_grad_workspace_bytes(rows, n)
     if workspace is None:
