@@ -303,23 +303,27 @@ __global__ __launch_bounds__(kMaxThreads) void rmsnorm_grad_long_kernel(const ui
   }
 }
 
-// dgamma = the sum of the G workspace rows: 64 columns a workgroup, 16 row
-// lanes of 4 columns a thread, the lanes added in order.
+// dgamma = the sum of the G workspace rows: 32 columns a workgroup, 32 row
+// lanes of 4 columns a thread, the lanes added in order.  (G is at most 256,
+// so a thread adds 8 rows: this is a matter of latency.)
 __global__ __launch_bounds__(256) void rmsnorm_dgamma_kernel(const float* part, int G, int64_t n, float* dgamma) {
-  __shared__ f32x4r lanes[16][16];
-  const int c = threadIdx.x & 15, l = threadIdx.x >> 4;
-  const int64_t col = (int64_t)blockIdx.x * 64 + 4 * c;
+  __shared__ f32x4r lanes[32][8];
+  const int c = threadIdx.x & 7, l = threadIdx.x >> 3;
+  const int64_t col = (int64_t)blockIdx.x * 32 + 4 * c;
   f32x4r s = {0.f, 0.f, 0.f, 0.f};
-  if (col < n)
-    for (int g = l; g < G; g += 16) s += *reinterpret_cast<const f32x4r*>(part + (int64_t)g * n + col);
+  if (col < n) {
+#pragma unroll 8
+    for (int g = l; g < G; g += 32) s += *reinterpret_cast<const f32x4r*>(part + (int64_t)g * n + col);
+  }
   lanes[l][c] = s;
   __syncthreads();
-  if (l == 0 && col < n) {
+  // 32 threads: one column each
+  const int64_t mine = (int64_t)blockIdx.x * 32 + threadIdx.x;
+  if (threadIdx.x < 32 && mine < n) {
+    float t = 0.f;
 #pragma unroll
-    for (int q = 1; q < 16; ++q) s += lanes[q][c];
-    // dgamma is only 4-byte aligned
-#pragma unroll
-    for (int e = 0; e < 4; ++e) dgamma[col + e] = s[e];
+    for (int q = 0; q < 32; ++q) t += lanes[q][threadIdx.x >> 2][threadIdx.x & 3];
+    dgamma[mine] = t;
   }
 }
 
@@ -401,7 +405,7 @@ hipError_t launch_rmsnorm_grad(const void* dy, const void* h, const void* gamma,
                         eps);
     if (e != hipSuccess) return e;
   }
-  return launch_kernel(rmsnorm_dgamma_kernel, dim3((unsigned)((n + 63) / 64)), dim3(256), stream, part, G, n, dgamma);
+  return launch_kernel(rmsnorm_dgamma_kernel, dim3((unsigned)((n + 31) / 32)), dim3(256), stream, part, G, n, dgamma);
 }
 
 }  // namespace gg
