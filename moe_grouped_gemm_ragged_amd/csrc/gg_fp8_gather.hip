@@ -185,9 +185,10 @@ __device__ __forceinline__ int block_scan(int v, int* wave_tot, int& before) {
 // which lie in as many experts; within an expert the rows ascend by token, so
 // the rows of one fraction of every expert come from about the same fraction
 // of the tokens.  Window i of `windows` is that fraction of every expert;
-// workgroup b runs on XCD b mod 8 and takes windows b mod 8, + 8, ..., so that
-// a window's tokens stay in that XCD's L2 for all their rows.  (Where a row
-// lies is exact; how well the windows fit the tokens only decides the speed.)
+// workgroup b runs on XCD b mod 8, and each XCD takes an eighth of the windows
+// one after the other, so that a window's tokens (and its neighbours', for the
+// fractions fit the tokens only roughly) stay in its L2 for all their rows.
+// Where a row lies is exact; how well the windows fit only decides the speed.
 template <int CH>
 __device__ __forceinline__ void copy_by_window(const uint8_t* src, const int32_t* row_slot, int32_t topk,
                                                int64_t tokens, const int32_t* offs, int32_t E, int64_t rows_cap,
@@ -213,7 +214,8 @@ __device__ __forceinline__ void copy_by_window(const uint8_t* src, const int32_t
   }
   __syncthreads();
   int turn = 0;
-  for (int w = block & 7; w < windows; w += 8) {
+  const int share = windows >> 3;       // windows is a multiple of 8
+  for (int w = (block & 7) * share; w < ((block & 7) + 1) * share; ++w) {
     // rows of this window before each expert's: two buffers in turn, see
     // RowSums in gg_norm.hip for why one barrier a window is enough
     int32_t* pref = s_pref[turn];
