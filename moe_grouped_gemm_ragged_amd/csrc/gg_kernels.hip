@@ -155,6 +155,7 @@ struct Operand {
 
 constexpr uint32_t kRsrcWord3 = 0x00020000u;   // gfx9 raw buffer, 32-bit dwords
 constexpr uint32_t kOutOfRange = 0x80000000u;  // an offset every record count here is below
+constexpr int kNonTemporal = 2;                // a buffer store's nt bit: the line is the first to leave the L2
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void* base, uint32_t nbytes) {
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, (int)nbytes, (int)kRsrcWord3);
@@ -1395,7 +1396,8 @@ __device__ __forceinline__ void store_tile_f32(uint8_t* cbase, uint32_t ldc_byte
 // free for the epilogue.
 constexpr int kSlabPitch = 64 * 4 + 16;
 
-template <int TMA, bool OUT_F32, bool SCALED>
+// AUX: cache bits of the bf16 stores.
+template <int TMA, bool OUT_F32, bool SCALED, int AUX = 0>
 __device__ __forceinline__ void store_tile_lds(uint8_t* cbase, uint32_t ldc_bytes, int rows, int cols,
                                                int wm, int wn, int lane, const floatx16 (&acc)[TM][TN],
                                                uint8_t* slab, float alpha, float beta,
@@ -1477,7 +1479,7 @@ __device__ __forceinline__ void store_tile_lds(uint8_t* cbase, uint32_t ldc_byte
       } else {
         u32x4 o = {pack_bf16x2(lo[0], lo[1]), pack_bf16x2(lo[2], lo[3]),
                    pack_bf16x2(hi[0], hi[1]), pack_bf16x2(hi[2], hi[3])};
-        __builtin_amdgcn_raw_buffer_store_b128(o, rs, voff, 0, 0);
+        __builtin_amdgcn_raw_buffer_store_b128(o, rs, voff, 0, AUX);
       }
       // one slab row group at a time (hoisting the prior-output loads of
       // all four would need 32 more registers)
@@ -1491,9 +1493,13 @@ __device__ __forceinline__ void store_tile_lds(uint8_t* cbase, uint32_t ldc_byte
 // The fp8 wgrad's fp32 epilogue: as store_tile_lds, but a store writes 256
 // contiguous bytes of each of 4 rows (store_tile_lds's lanes hold 32 bytes, as
 // bf16 packing needs them, and store two pieces of 16 with gaps that the next
-// store fills): 128 experts of 512 rows, k 2048, n 1536 621 -> 580 us.  Slab
-// rows are 256 bytes, the 16-byte chunk c of row r at position c ^ (r mod 16),
-// which keeps both accesses conflict-free.
+// store fills): 128 experts of 512 rows, k 2048, n 1536 621 -> 580 us.  The
+// stores are non-temporal: dW is larger than the L2s and nothing here reads it
+// again, while x and dY are shared by an expert's tiles: 128 experts of 128
+// rows 340 -> 300 us (bf16 dW 240 -> 212), of 512 575 -> 565, longer experts
+// and the masked layout unchanged.  Slab rows are 256 bytes, the 16-byte chunk
+// c of row r at position c ^ (r mod 16), which keeps both accesses
+// conflict-free.
 template <bool SCALED>
 __device__ __forceinline__ void store_tile_x8(uint8_t* cbase, uint32_t ldc_bytes, int rows, int cols, int wm, int wn,
                                               int lane, const floatx16 (&acc)[TM][TN], uint8_t* slab, float alpha,
@@ -1526,7 +1532,7 @@ __device__ __forceinline__ void store_tile_x8(uint8_t* cbase, uint32_t ldc_bytes
         if (beta != 0.0f)
           v = v + __builtin_bit_cast(floatx4, __builtin_amdgcn_raw_buffer_load_b128(rs, voff, 0, 0)) * beta;
       }
-      __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), rs, voff, 0, 0);
+      __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), rs, voff, 0, kNonTemporal);
       if constexpr (SCALED) __builtin_amdgcn_sched_barrier(0);
     }
     // the next block row rewrites the slab: wait for this row's reads
@@ -2116,6 +2122,7 @@ __global__ __launch_bounds__(NT, 1) void grouped_gemm_kernel(Params p) {
       stage_barrier();
       // each wave stages through its own 16 KB of the (idle) stage buffers
       uint8_t* slab = smem + wave * (STAGE_BYTES / 2);
+      [[maybe_unused]] constexpr int kAux = is_x8(MODE) ? kNonTemporal : 0;   // see store_tile_x8
       if constexpr (is_silu(MODE)) {
         if (half)
           store_tile_silu<2, OUT_F32>(cur.cbase, cur.ldc_bytes, cur.rows, cur.cols, wave, wm, wn, lane,
@@ -2130,18 +2137,18 @@ __global__ __launch_bounds__(NT, 1) void grouped_gemm_kernel(Params p) {
           store_tile_x8<false>(cur.cbase, cur.ldc_bytes, cur.rows, cur.cols, wm, wn, lane, acc, slab, 1.0f, 0.0f);
       } else if (scaled) {
         if (half)
-          store_tile_lds<2, OUT_F32, true>(cur.cbase, cur.ldc_bytes, cur.rows, cur.cols, wm, wn, lane,
-                                           acc, slab, p.alpha, p.beta, cur.bias, cur.bscale);
+          store_tile_lds<2, OUT_F32, true, kAux>(cur.cbase, cur.ldc_bytes, cur.rows, cur.cols, wm, wn, lane,
+                                                 acc, slab, p.alpha, p.beta, cur.bias, cur.bscale);
         else
-          store_tile_lds<TM, OUT_F32, true>(cur.cbase, cur.ldc_bytes, cur.rows, cur.cols, wm, wn, lane,
-                                            acc, slab, p.alpha, p.beta, cur.bias, cur.bscale);
+          store_tile_lds<TM, OUT_F32, true, kAux>(cur.cbase, cur.ldc_bytes, cur.rows, cur.cols, wm, wn, lane,
+                                                  acc, slab, p.alpha, p.beta, cur.bias, cur.bscale);
       } else if constexpr (!OUT_F32 || is_fp8(MODE) || STAGED_F32) {
         if (half)
-          store_tile_lds<2, OUT_F32, false>(cur.cbase, cur.ldc_bytes, cur.rows, cur.cols, wm, wn, lane,
-                                            acc, slab, 1.0f, 0.0f);
+          store_tile_lds<2, OUT_F32, false, kAux>(cur.cbase, cur.ldc_bytes, cur.rows, cur.cols, wm, wn, lane,
+                                                  acc, slab, 1.0f, 0.0f);
         else
-          store_tile_lds<TM, OUT_F32, false>(cur.cbase, cur.ldc_bytes, cur.rows, cur.cols, wm, wn, lane,
-                                             acc, slab, 1.0f, 0.0f);
+          store_tile_lds<TM, OUT_F32, false, kAux>(cur.cbase, cur.ldc_bytes, cur.rows, cur.cols, wm, wn, lane,
+                                                   acc, slab, 1.0f, 0.0f);
       }
       prev_stores = 0;
       // the next tile's first loads overwrite these arrays
