@@ -652,7 +652,7 @@ __device__ __attribute__((always_inline)) inline void mainloop_x8(
     uint8_t* __restrict__ s0, uint8_t* __restrict__ s1, uint8_t* __restrict__ s2, uint8_t* __restrict__ s3,
     const uint8_t* __restrict__ a_origin, const uint8_t* __restrict__ b_origin, const uint8_t* __restrict__ sa,
     int64_t tile_bytes, uint32_t sc_left, Operand A, Operand B, int tid, int wave, const FragAddr& faa,
-    const FragAddr& fab, floatx16 (&acc)[TM][TN], int prev_stores, X8Regs& x) {
+    const FragAddr& fab, floatx16 (&acc)[TM][TN], X8Regs& x) {
   A.origin = a_origin;
   B.origin = b_origin;
   const int nk = (A.red + BK - 1) / BK;
@@ -732,10 +732,7 @@ __device__ __attribute__((always_inline)) inline void mainloop_x8(
     }
 #undef GG_PP_STAGE0
   } else {
-    // stage 0 of B landed (stages 1, 2 in flight, and the previous tile's
-    // stores where they went out behind these loads)
-    if (prev_stores == stores_f32<TM>()) pp_sync<8 + stores_f32<TM>()>(rg);
-    else pp_sync<8>(rg);
+    pp_sync<8>(rg);                                  // stage 0 of B landed (1, 2 in flight)
 #define GG_PP_STAGE1(BC, BP, KT)                                                                  \
   {                                                                                               \
     __builtin_amdgcn_sched_barrier(0);                                                            \
@@ -2065,7 +2062,7 @@ __global__ __launch_bounds__(NT, 1) void grouped_gemm_kernel(Params p) {
     // still in flight behind their prologue loads
     if constexpr (is_x8(MODE)) {
       mainloop_x8<WIDE>(sa0, sa1, sa2, sa3, cur.A.origin, cur.B.origin, cur.sa, p.k / 128 * 256, cur.sa_left, cur.A,
-                        cur.B, tid, wave, faa, fab, acc, prev_stores, x8);
+                        cur.B, tid, wave, faa, fab, acc, x8);
     } else if constexpr (is_fp8(MODE)) {
       const uint32_t sc_bytes = (uint32_t)(p.k / 128 * 256);
       if (half)
