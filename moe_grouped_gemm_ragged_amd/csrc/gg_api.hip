@@ -601,6 +601,7 @@ gg_status gg_fp8_masked_forward(const void* x, const void* x_scales, const void*
 static gg_status fp8_wgrad_run(bool masked, const void* x, const void* xs, const void* dy, const int32_t* groups,
                                void* dw, gg_dtype dw_dtype, int64_t rows, int64_t k, int64_t n, int32_t num_groups,
                                float alpha, float beta, void* stream) {
+  if (rows == 0) x = xs = dy = groups;      // nothing is read: operands without rows may be NULL
   gg_status s = check(x, dy, groups, dw, dw_dtype, rows, k, n, num_groups);
   if (s != GG_OK) return s;
   if (!xs) return fail(GG_ERR_NULL_PTR, "a required pointer is NULL");

@@ -118,6 +118,12 @@ def test_no_rows_need_no_memory(lib, name, defaults, case):
     assert run(name, defaults, case) != 1, gg.last_error()
 
 
+@pytest.mark.parametrize("name", ["gg_fp8_wgrad", "gg_fp8_masked_wgrad"])
+def test_fp8_wgrad_without_rows_needs_no_operands(lib, name):
+    assert run(name, WGRAD, dict(m=0, x=0, xs=0, dy=0)) != 1, gg.last_error()
+    assert run(name, WGRAD, dict(m=0, offs=0)) == 1 and run(name, WGRAD, dict(m=0, dw=0)) == 1
+
+
 def bf(*shape):
     return torch.zeros(*shape, dtype=torch.bfloat16)
 

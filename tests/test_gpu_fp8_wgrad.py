@@ -141,3 +141,23 @@ def test_fp8_wgrad_in_a_graph():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, want), trial
+
+
+def test_fp8_wgrad_without_rows():
+    """No rows at all (and so no memory behind x, its scales and dY): dW is 0,
+    or what beta leaves of it."""
+    dev = device()
+    groups = torch.zeros(5, dtype=torch.int32, device=dev)
+    say("fp8_wgrad without rows")
+    for masked in (False, True):
+        lead = (5, 0) if masked else (0,)
+        x, dy = torch.empty(*lead, 384, dtype=U8, device=dev), torch.empty(*lead, 72, dtype=BF, device=dev)
+        scales = torch.empty(gg.fp8_scale_bytes(gg.GG_FP8_ACT_MASKED if masked else gg.GG_FP8_ACT_RAGGED, 0, 384, 5),
+                             dtype=U8, device=dev)
+        for dtype in (torch.float32, BF):
+            out = torch.full((5, 384, 72), 3.0, dtype=dtype, device=dev)
+            run(masked, x, scales, dy, groups, out=out)
+            assert bool((out == 0).all())
+            out.fill_(3.0)
+            run(masked, x, scales, dy, groups, out=out, beta=0.5)
+            assert bool((out == 1.5).all())
