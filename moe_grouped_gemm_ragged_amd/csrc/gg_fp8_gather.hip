@@ -29,7 +29,7 @@ constexpr int kTile = 256;      // rows of a packed scale tile
 constexpr int kKb = 8;          // k-blocks a wave packs at a time
 // Workgroups a compute unit at most: copying rows in order; copying by
 // windows, where fewer keep closer together (8195 tokens of 7168 bytes to 8
-// experts each: 113 us with 2, 119 with 4, 131 with 8); packing scales (first
+// experts each: 108 us with 2, 114 with 4, 120 with 8); packing scales (first
 // in the grid: few bytes, long latency).
 constexpr int kRowBlocks = 8;
 constexpr int kWindowBlocks = 2;
@@ -330,11 +330,13 @@ hipError_t launch_fp8_gather_rows(const void* src, const void* src_scales, const
   const int64_t kib = (k + 1023) / 1024;
   const int ch = kib <= 1 ? 1 : kib <= 2 ? 2 : kib <= 4 ? 4 : 8;
   // Rows by windows where tokens are read several times and a large src would
-  // come from memory each time: 8195 x 7168 to 8 of 256 experts 113 us (in
-  // order 152), 8192 x 2048 to 8 of 128 28.4 us (in order 41.8).
+  // come from memory each time: 8195 x 7168 to 8 of 256 experts 108 us (in
+  // order 152), 8192 x 2048 to 8 of 128 28.6 us (in order 41.8).  (With fewer
+  // rows than tokens most tokens are read once at most, and the windows, as
+  // many as src is long, would hold next to nothing each.)
   const int64_t bytes = tokens * k;
-  const int windows = topk > 1 && bytes > kWindowedBytes
-                          ? (int)((bytes + 8 * kWindowBytes - 1) / (8 * kWindowBytes) * 8) : 0;
+  const bool windowed = topk > 1 && bytes > kWindowedBytes && rows_cap > tokens;
+  const int windows = windowed ? (int)((bytes + 8 * kWindowBytes - 1) / (8 * kWindowBytes) * 8) : 0;
   const int64_t per = kWaves * (kUnits / ch);
   const int64_t rows_want = (rows_cap + per - 1) / per;
   const int64_t rows_most = (windows ? kWindowBlocks : kRowBlocks) * (int64_t)num_cus;

@@ -204,6 +204,24 @@ def test_fp8_gather_rows_of_many_tokens(tokens, topk, e, k, align, pad, drop):
     assert torch.equal(packed[:n], same[:n])
 
 
+def test_fp8_gather_rows_fewer_than_tokens():
+    """Room for fewer rows than there are tokens, of a src of 60 MB."""
+    dev = device()
+    offs, row_slot, _ = routing(5, 8000, 4, 16, 8, True)
+    row_slot, k = row_slot[:333].contiguous(), 7552
+    src = torch.randint(0, 256, (8000, k), device=dev, dtype=U8)
+    scales = torch.randint(1, 255, (8000, k // 128), device=dev, dtype=U8)
+    say("fp8_gather_rows with little room")
+    out, packed = gg.fp8_gather_rows(src, scales, row_slot, 4, offs)
+    slot = row_slot.long()
+    assert torch.equal(out, torch.where((slot >= 0)[:, None], src[slot.clamp(min=0) // 4], torch.zeros_like(out)))
+    raw = torch.where((slot >= 0)[:, None], scales[slot.clamp(min=0) // 4], torch.full((1, 1), 127, dtype=U8, device=dev))
+    same = gg.fp8_pack_scales(gg.GG_FP8_ACT_RAGGED, raw.contiguous(), offs, 333, k, 16)
+    ends = [min(int(v), 333) for v in offs]
+    n = sum(-(-(b - a) // 256) for a, b in zip([0] + ends, ends)) * (k // 128) * 256
+    assert torch.equal(packed[:n], same[:n])
+
+
 def test_fp8_gather_rows_feeds_the_packed_layout():
     """The scales are those that gg_fp8_pack_scales writes for the gathered rows."""
     dev = device()
