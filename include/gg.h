@@ -582,7 +582,10 @@ gg_status gg_fp8_masked_wgrad(const void* x, const void* x_scales,
  *   y         [rows, n]  bf16, or NULL
  *   y8, y8_scales        e4m3 rows of y (n a multiple of 128), or both NULL
  * At least one output must be given.  eps >= 0; a row of zeros with eps = 0
- * gives NaN, as the formula does.
+ * gives NaN, as the formula does.  The squares are summed in fp32: a row of
+ * values beyond 2^64 / sqrt(n), or below 2^-63 with eps = 0, leaves its range
+ * and comes out as 0, inexact or not finite.  An infinity or NaN reaches its
+ * own row only.
  *
  * gg_rmsnorm_grad -- its gradient at h.  With rho = 1 / sqrt(mean(h^2) + eps),
  * u = h rho and p = dy gamma:

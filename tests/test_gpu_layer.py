@@ -103,6 +103,31 @@ def test_rmsnorm_grad(rows, n, res):
     assert torch.equal(dx, again[0]) and torch.equal(dgamma, again[1]), "two calls differ"
 
 
+def test_rmsnorm_rows_that_are_not_finite():
+    """An infinity or a NaN changes its own row only (of the gradient: and
+    dgamma), and comes out as the formula has it: rho is 0 or NaN."""
+    device()
+    g = gen(17)
+    for rows, n in ((11, 128), (6, 1024), (4, 33024)):
+        x, gamma, dy = randn(g, rows, n), randn(g, n), randn(g, rows, n)
+        good = [t.clone() for t in gg.fp8_rmsnorm(x, gamma, with_bf16=True) if t is not None]
+        dx_good, _ = gg.rmsnorm_grad(dy, x, gamma)
+        x[1, 5], x[2, n - 1] = float("inf"), float("nan")
+        say("rmsnorm of an infinity and a NaN", rows, n)
+        codes, scales, _, y = gg.fp8_rmsnorm(x, gamma, with_bf16=True)
+        dx, dgamma = gg.rmsnorm_grad(dy, x, gamma)
+        torch.cuda.synchronize()
+        rest = [i for i in range(rows) if i not in (1, 2)]
+        for a, b in zip((codes, scales, y), good):
+            assert torch.equal(a[rest].view(U8), b[rest].view(U8))
+        assert torch.equal(dx[rest], dx_good[rest])
+        assert bool(torch.isnan(y[2]).all()) and bool(((codes[2] & 0x7F) == 0x7F).all())
+        at = torch.arange(n, device="cuda") == 5
+        assert torch.equal(torch.isnan(y[1]), at) and bool((y[1][~at] == 0).all())
+        assert torch.equal((codes[1] & 0x7F) == 0x7F, at) and bool((scales[1:3] == 127).all())
+        assert bool(torch.isnan(dx[2]).all()) and bool(torch.isnan(dgamma).all())
+
+
 def test_rmsnorm_grad_no_rows_in_place_and_differences():
     device()
     g = gen(5)
