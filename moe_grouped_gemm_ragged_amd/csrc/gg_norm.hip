@@ -16,7 +16,10 @@
 // the gradient of x and of residual alike.
 //
 // Both are bound by memory: one read of every operand, one write of every
-// output, the row held in registers in between.
+// output, the row held in registers in between.  16384 x 7168 with a residual
+// to h and e4m3 rows 150-160 us (5.1-5.5 TB/s; the counters show 824 MB moved,
+// of 823 needed); the gradient of 8192 x 6144 with dh 74.5 + 4.8 us (5.1 TB/s;
+// 409 MB of 403).  A single row of 2048 takes 2.7 us, which is one launch.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
