@@ -1400,8 +1400,7 @@ __device__ __forceinline__ void store_tile_f32(uint8_t* cbase, uint32_t ldc_byte
 // free for the epilogue.
 constexpr int kSlabPitch = 64 * 4 + 16;
 
-// AUX: cache bits of the bf16 stores.
-template <int TMA, bool OUT_F32, bool SCALED, int AUX = 0>
+template <int TMA, bool OUT_F32, bool SCALED>
 __device__ __forceinline__ void store_tile_lds(uint8_t* cbase, uint32_t ldc_bytes, int rows, int cols,
                                                int wm, int wn, int lane, const floatx16 (&acc)[TM][TN],
                                                uint8_t* slab, float alpha, float beta,
@@ -1483,7 +1482,7 @@ __device__ __forceinline__ void store_tile_lds(uint8_t* cbase, uint32_t ldc_byte
       } else {
         u32x4 o = {pack_bf16x2(lo[0], lo[1]), pack_bf16x2(lo[2], lo[3]),
                    pack_bf16x2(hi[0], hi[1]), pack_bf16x2(hi[2], hi[3])};
-        __builtin_amdgcn_raw_buffer_store_b128(o, rs, voff, 0, AUX);
+        __builtin_amdgcn_raw_buffer_store_b128(o, rs, voff, 0, 0);
       }
       // one slab row group at a time (hoisting the prior-output loads of
       // all four would need 32 more registers)
@@ -1497,14 +1496,18 @@ __device__ __forceinline__ void store_tile_lds(uint8_t* cbase, uint32_t ldc_byte
 // The fp8 wgrad's fp32 epilogue: as store_tile_lds, but a store writes 256
 // contiguous bytes of each of 4 rows (store_tile_lds's lanes hold 32 bytes, as
 // bf16 packing needs them, and store two pieces of 16 with gaps that the next
-// store fills): 128 experts of 512 rows, k 2048, n 1536 621 -> 580 us.  The
-// stores are non-temporal: dW is larger than the L2s and nothing here reads it
-// again, while x and dY are shared by an expert's tiles: 128 experts of 128
-// rows 340 -> 300 us (bf16 dW 240 -> 212), of 512 575 -> 565, longer experts
-// and the masked layout unchanged.  Slab rows are 256 bytes, the 16-byte chunk
-// c of row r at position c ^ (r mod 16), which keeps both accesses
-// conflict-free.
-template <bool SCALED>
+// store fills): 128 experts of 512 rows, k 2048, n 1536 621 -> 580 us.  Slab
+// rows are 256 bytes, the 16-byte chunk c of row r at position c ^ (r mod 16),
+// which keeps both accesses conflict-free.
+//
+// NT: non-temporal stores, for dW rows that begin on cache lines, so that every
+// store fills whole ones: dW is larger than the L2s and nothing here reads it
+// again, while x and dY are shared by an expert's tiles.  128 experts of 128
+// rows, k 2048: n 1536 340 -> 300 us, but n 1000, whose lines the stores fill in
+// parts, 264 -> 349; 256 experts, k 7168, n 2048 2774 -> 2676; 512 rows and more
+// within 2 %.  (bf16 dW gains in one place what it loses in another and goes
+// out plainly.)
+template <bool SCALED, bool NT>
 __device__ __forceinline__ void store_tile_x8(uint8_t* cbase, uint32_t ldc_bytes, int rows, int cols, int wm, int wn,
                                               int lane, const floatx16 (&acc)[TM][TN], uint8_t* slab, float alpha,
                                               float beta) {
@@ -1536,7 +1539,7 @@ __device__ __forceinline__ void store_tile_x8(uint8_t* cbase, uint32_t ldc_bytes
         if (beta != 0.0f)
           v = v + __builtin_bit_cast(floatx4, __builtin_amdgcn_raw_buffer_load_b128(rs, voff, 0, 0)) * beta;
       }
-      __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), rs, voff, 0, kNonTemporal);
+      __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), rs, voff, 0, NT ? kNonTemporal : 0);
       if constexpr (SCALED) __builtin_amdgcn_sched_barrier(0);
     }
     // the next block row rewrites the slab: wait for this row's reads
@@ -2126,7 +2129,6 @@ __global__ __launch_bounds__(NT, 1) void grouped_gemm_kernel(Params p) {
       stage_barrier();
       // each wave stages through its own 16 KB of the (idle) stage buffers
       uint8_t* slab = smem + wave * (STAGE_BYTES / 2);
-      [[maybe_unused]] constexpr int kAux = is_x8(MODE) ? kNonTemporal : 0;   // see store_tile_x8
       if constexpr (is_silu(MODE)) {
         if (half)
           store_tile_silu<2, OUT_F32>(cur.cbase, cur.ldc_bytes, cur.rows, cur.cols, wave, wm, wn, lane,
@@ -2136,23 +2138,27 @@ __global__ __launch_bounds__(NT, 1) void grouped_gemm_kernel(Params p) {
                                        acc, smem);
       } else if constexpr (is_x8(MODE) && OUT_F32) {
         if (scaled)
-          store_tile_x8<true>(cur.cbase, cur.ldc_bytes, cur.rows, cur.cols, wm, wn, lane, acc, slab, p.alpha, p.beta);
+          store_tile_x8<true, false>(cur.cbase, cur.ldc_bytes, cur.rows, cur.cols, wm, wn, lane, acc, slab, p.alpha,
+                                     p.beta);
+        else if (((cur.ldc_bytes | (uint32_t)reinterpret_cast<uintptr_t>(cur.cbase)) & 127u) == 0u)
+          store_tile_x8<false, true>(cur.cbase, cur.ldc_bytes, cur.rows, cur.cols, wm, wn, lane, acc, slab, 1.0f, 0.0f);
         else
-          store_tile_x8<false>(cur.cbase, cur.ldc_bytes, cur.rows, cur.cols, wm, wn, lane, acc, slab, 1.0f, 0.0f);
+          store_tile_x8<false, false>(cur.cbase, cur.ldc_bytes, cur.rows, cur.cols, wm, wn, lane, acc, slab, 1.0f,
+                                      0.0f);
       } else if (scaled) {
         if (half)
-          store_tile_lds<2, OUT_F32, true, kAux>(cur.cbase, cur.ldc_bytes, cur.rows, cur.cols, wm, wn, lane,
-                                                 acc, slab, p.alpha, p.beta, cur.bias, cur.bscale);
+          store_tile_lds<2, OUT_F32, true>(cur.cbase, cur.ldc_bytes, cur.rows, cur.cols, wm, wn, lane,
+                                           acc, slab, p.alpha, p.beta, cur.bias, cur.bscale);
         else
-          store_tile_lds<TM, OUT_F32, true, kAux>(cur.cbase, cur.ldc_bytes, cur.rows, cur.cols, wm, wn, lane,
-                                                  acc, slab, p.alpha, p.beta, cur.bias, cur.bscale);
+          store_tile_lds<TM, OUT_F32, true>(cur.cbase, cur.ldc_bytes, cur.rows, cur.cols, wm, wn, lane,
+                                            acc, slab, p.alpha, p.beta, cur.bias, cur.bscale);
       } else if constexpr (!OUT_F32 || is_fp8(MODE) || STAGED_F32) {
         if (half)
-          store_tile_lds<2, OUT_F32, false, kAux>(cur.cbase, cur.ldc_bytes, cur.rows, cur.cols, wm, wn, lane,
-                                                  acc, slab, 1.0f, 0.0f);
+          store_tile_lds<2, OUT_F32, false>(cur.cbase, cur.ldc_bytes, cur.rows, cur.cols, wm, wn, lane,
+                                            acc, slab, 1.0f, 0.0f);
         else
-          store_tile_lds<TM, OUT_F32, false, kAux>(cur.cbase, cur.ldc_bytes, cur.rows, cur.cols, wm, wn, lane,
-                                                   acc, slab, 1.0f, 0.0f);
+          store_tile_lds<TM, OUT_F32, false>(cur.cbase, cur.ldc_bytes, cur.rows, cur.cols, wm, wn, lane,
+                                             acc, slab, 1.0f, 0.0f);
       }
       prev_stores = 0;
       // the next tile's first loads overwrite these arrays

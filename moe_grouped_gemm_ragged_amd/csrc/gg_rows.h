@@ -39,8 +39,9 @@ __device__ __forceinline__ u32x4r load16(const void* p) { return *static_cast<co
 // call where bandwidth counts, and the operands still to be read keep their
 // place.  Against ordinary stores: norm of 16384 x 7168 156 -> 153 us, its
 // gradient at 8192 x 6144 88.9 -> 86.5, combine gradient 8192 x 8 x 2048 117 ->
-// 115, SiLU-mul gradient of 65536 x 768 96.7 -> 93.7; the GEMM that reads them
-// next is within 1 % either way.
+// 115, SiLU-mul gradient of 65536 x 768 96.7 -> 93.7; rows that are no whole
+// cache lines (n 1000, 2056, 7176) between 4 % faster and 6 % slower; the GEMM
+// that reads them next is within 1 % either way.
 __device__ __forceinline__ void store16(void* p, const u32x4r& v) {
   __builtin_nontemporal_store(v, static_cast<u32x4r*>(p));
 }
