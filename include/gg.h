@@ -3,8 +3,9 @@
  * (gfx950): the bf16 passes below, then their scaled and accumulating
  * forms, the masked backward, the SiLU-mul gate/up forward, the grouped
  * bias and its backward, the [E, N, K] weight layout, the steps that
- * produce the grouped layout (offsets, routing, gather, combine), and the
- * fp8 block-scaled forward.
+ * produce the grouped layout (offsets, routing, gather, combine), the fp8
+ * block-scaled forward, and the steps of a layer that keeps its activations
+ * in 8 bits (norm, 8-bit gather, combine gradient, SiLU-mul rows, dW).
  *
  * The operation (PyTorch issue #152668, "Easy repro scenario", and its
  * backward): a 2-D activation X[M,K], a packed 3-D weight W[E,K,N] and int32
@@ -23,7 +24,8 @@
  * ------------------------------------
  *  - Tensors are bf16 (uint16 storage), row-major and densely packed, in
  *    device memory the CALLER owns.  The library allocates nothing, frees
- *    nothing, needs no workspace, never copies device -> host and never
+ *    nothing, needs no workspace but those that gg_route and gg_rmsnorm_grad
+ *    take as an argument, never copies device -> host and never
  *    synchronises: it validates the arguments on the host, then enqueues
  *    kernels on `stream` (a hipStream_t; NULL = the default stream) and
  *    returns.  Group sizes stay on the device (TransformerEngine PR #3542,
