@@ -823,15 +823,21 @@ def _raw_stream(index):
 
 
 def _shaped(t, name, dtype, shape, device, like=None):
-    """``t`` checked against a shape, or a new tensor of it (that ``like``
-    has too, where there is one: the cheaper call)."""
+    """``t`` checked against a shape (of up to 3 dimensions), or a new tensor
+    of it (that ``like`` has too, where there is one: the cheapest call)."""
+    torch = _torch()
     if t is None:
-        torch = _torch()
-        return torch.empty(shape, dtype=dtype, device=device) if like is None else torch.empty_like(like)
+        if like is not None:
+            return torch.empty_like(like)
+        # (with its strides: 0.4 us less than torch.empty, of a small call's 9 to 13)
+        strides = (shape[1], 1) if len(shape) == 2 else (1,) if len(shape) == 1 else (shape[1] * shape[2], shape[2], 1)
+        return torch.empty_strided(shape, strides, dtype=dtype, device=device)
+    # everything at once where all is well (half the time of naming what is not)
+    if (isinstance(t, torch.Tensor) and t.shape == shape and t.dtype == dtype and t.device == device
+            and t.is_contiguous()):
+        return t
     _check(t, name, dtype, len(shape), device)
-    if t.shape != shape:
-        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    return t
+    raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
 
 
 def _ptr(t):
@@ -904,7 +910,7 @@ def rmsnorm_grad(dy, h, gamma, dh=None, eps=1e-6, out=None, dgamma=None, workspa
     dgamma = _shaped(dgamma, "dgamma", torch.float32, (n,), dev)
     need = rmsnorm_grad_workspace_bytes(rows, n)
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        workspace = _shaped(None, "workspace", torch.uint8, (need,), dev)
     _check(workspace, "workspace", torch.uint8, 1, dev)
     if workspace.numel() < need:
         raise ValueError(f"workspace must hold {need} bytes")
@@ -958,7 +964,7 @@ def combine_rows_grad(dout, y, slot_row, row_slot, offs, topk, weights=None, out
         if y is None:
             raise ValueError("the gradient of the weights needs y")
         _shaped(y, "y", torch.bfloat16, (cap, n), dev)
-        dw = torch.empty((tokens, topk), dtype=torch.float32, device=dev)
+        dw = _shaped(None, "dweights", torch.float32, (tokens, topk), dev)
     out = _shaped(out, "out", torch.bfloat16, (cap, n), dev)
     _launch("gg_combine_rows_grad", dev, _ptr(dout), _dtype_code(dout.dtype), _ptr(y) if with_weights else None, n,
             _ptr(slot_row), _ptr(row_slot), _ptr(offs), e, _ptr(weights), topk, tokens, cap, _ptr(out), _ptr(dw))
