@@ -1400,7 +1400,8 @@ __device__ __forceinline__ void store_tile_f32(uint8_t* cbase, uint32_t ldc_byte
 // free for the epilogue.
 constexpr int kSlabPitch = 64 * 4 + 16;
 
-template <int TMA, bool OUT_F32, bool SCALED>
+// AUX: cache bits of the bf16 stores.
+template <int TMA, bool OUT_F32, bool SCALED, int AUX = 0>
 __device__ __forceinline__ void store_tile_lds(uint8_t* cbase, uint32_t ldc_bytes, int rows, int cols,
                                                int wm, int wn, int lane, const floatx16 (&acc)[TM][TN],
                                                uint8_t* slab, float alpha, float beta,
@@ -1482,7 +1483,7 @@ __device__ __forceinline__ void store_tile_lds(uint8_t* cbase, uint32_t ldc_byte
       } else {
         u32x4 o = {pack_bf16x2(lo[0], lo[1]), pack_bf16x2(lo[2], lo[3]),
                    pack_bf16x2(hi[0], hi[1]), pack_bf16x2(hi[2], hi[3])};
-        __builtin_amdgcn_raw_buffer_store_b128(o, rs, voff, 0, 0);
+        __builtin_amdgcn_raw_buffer_store_b128(o, rs, voff, 0, AUX);
       }
       // one slab row group at a time (hoisting the prior-output loads of
       // all four would need 32 more registers)
@@ -1505,8 +1506,9 @@ __device__ __forceinline__ void store_tile_lds(uint8_t* cbase, uint32_t ldc_byte
 // again, while x and dY are shared by an expert's tiles.  128 experts of 128
 // rows, k 2048: n 1536 340 -> 300 us, but n 1000, whose lines the stores fill in
 // parts, 264 -> 349; 256 experts, k 7168, n 2048 2774 -> 2676; 512 rows and more
-// within 2 %.  (bf16 dW gains in one place what it loses in another and goes
-// out plainly.)
+// within 2 %.  bf16 dW (store_tile_lds) by the same rule: 128 rows, n 1536 252
+// -> 220 us, 64 masked experts of at most 256 rows, 768 x 2048 67 -> 64, 256
+// experts, k 7168, n 2048 2147 -> 2250; n 1032 390, 515 without the rule.
 template <bool SCALED, bool NT>
 __device__ __forceinline__ void store_tile_x8(uint8_t* cbase, uint32_t ldc_bytes, int rows, int cols, int wm, int wn,
                                               int lane, const floatx16 (&acc)[TM][TN], uint8_t* slab, float alpha,
@@ -2129,6 +2131,9 @@ __global__ __launch_bounds__(NT, 1) void grouped_gemm_kernel(Params p) {
       stage_barrier();
       // each wave stages through its own 16 KB of the (idle) stage buffers
       uint8_t* slab = smem + wave * (STAGE_BYTES / 2);
+      // rows of the output begin on cache lines (see store_tile_x8)
+      [[maybe_unused]] const bool whole_lines =
+          ((cur.ldc_bytes | (uint32_t)reinterpret_cast<uintptr_t>(cur.cbase)) & 127u) == 0u;
       if constexpr (is_silu(MODE)) {
         if (half)
           store_tile_silu<2, OUT_F32>(cur.cbase, cur.ldc_bytes, cur.rows, cur.cols, wave, wm, wn, lane,
@@ -2140,7 +2145,7 @@ __global__ __launch_bounds__(NT, 1) void grouped_gemm_kernel(Params p) {
         if (scaled)
           store_tile_x8<true, false>(cur.cbase, cur.ldc_bytes, cur.rows, cur.cols, wm, wn, lane, acc, slab, p.alpha,
                                      p.beta);
-        else if (((cur.ldc_bytes | (uint32_t)reinterpret_cast<uintptr_t>(cur.cbase)) & 127u) == 0u)
+        else if (whole_lines)
           store_tile_x8<false, true>(cur.cbase, cur.ldc_bytes, cur.rows, cur.cols, wm, wn, lane, acc, slab, 1.0f, 0.0f);
         else
           store_tile_x8<false, false>(cur.cbase, cur.ldc_bytes, cur.rows, cur.cols, wm, wn, lane, acc, slab, 1.0f,
@@ -2152,6 +2157,9 @@ __global__ __launch_bounds__(NT, 1) void grouped_gemm_kernel(Params p) {
         else
           store_tile_lds<TM, OUT_F32, true>(cur.cbase, cur.ldc_bytes, cur.rows, cur.cols, wm, wn, lane,
                                             acc, slab, p.alpha, p.beta, cur.bias, cur.bscale);
+      } else if (is_x8(MODE) && whole_lines) {
+        store_tile_lds<TM, OUT_F32, false, kNonTemporal>(cur.cbase, cur.ldc_bytes, cur.rows, cur.cols, wm, wn, lane,
+                                                         acc, slab, 1.0f, 0.0f);
       } else if constexpr (!OUT_F32 || is_fp8(MODE) || STAGED_F32) {
         if (half)
           store_tile_lds<2, OUT_F32, false>(cur.cbase, cur.ldc_bytes, cur.rows, cur.cols, wm, wn, lane,
