@@ -161,3 +161,25 @@ def test_fp8_wgrad_without_rows():
             out.fill_(3.0)
             run(masked, x, scales, dy, groups, out=out, beta=0.5)
             assert bool((out == 1.5).all())
+
+
+@pytest.mark.parametrize("sizes,k,n,max_m", [([300, 0, 70], 384, 200, None), ([600, 0, 257], 256, 512, 640)])
+@pytest.mark.parametrize("dtype", [torch.float32, BF])
+def test_fp8_wgrad_output_off_the_cache_lines(sizes, k, n, max_m, dtype):
+    """An output that begins 16 bytes into a line, overwritten and
+    accumulated into; what lies before and behind it stays."""
+    codes, packed, dy, groups, xb = operands(sizes, k, n, n, 0, max_m)
+    masked, e = max_m is not None, len(sizes)
+    pad = 16 // (torch.finfo(dtype).bits // 8)
+    whole = torch.randn(e * k * n + 2 * pad, device="cuda").to(dtype)
+    before = whole.clone()
+    out = whole[pad:-pad].view(e, k, n)
+    assert out.data_ptr() % 128 == 16 and out.is_contiguous()
+    say("fp8_wgrad off the lines", sizes, k, n, dtype)
+    run(masked, codes, packed, dy, groups, out=out, alpha=0.5, beta=1.0)
+    want = bf16(masked, xb, dy, groups, out=before[pad:-pad].view(e, k, n).clone(), alpha=0.5, beta=1.0)
+    assert torch.equal(out, want)
+    run(masked, codes, packed, dy, groups, out=out)
+    assert torch.equal(out, bf16(masked, xb, dy, groups, out_dtype=dtype))
+    assert torch.equal(run(masked, codes, packed, dy, groups, out_dtype=dtype), out), "and on the lines"
+    assert torch.equal(whole[:pad], before[:pad]) and torch.equal(whole[-pad:], before[-pad:])
