@@ -1,4 +1,5 @@
-"""GPU tests of the layer steps where an operand passes 4 GB and 2^31 elements:
+"""GPU tests of the layer steps where an operand passes 4 GB and 2^31 elements,
+or has more rows than a launch has workgroups:
 the last rows (and a sample of the others) against the plain fp64 forms, or,
 where the operator only moves bytes, all of them; dW from 8-bit rows against
 exact integers."""
@@ -47,6 +48,39 @@ def test_norm_and_gradient_over_4gb():
         size += t.abs().sum(0)
     # the bound of layer_ref.rmsnorm_grad, whose sum runs over all rows
     ref.close(dgamma, total.cpu(), total.cpu().abs() * 2.0 ** -24 + size.cpu() * (ROWS + N / 2 + 16) * ref.U32, "dgamma")
+
+
+@pytest.mark.parametrize("rows,n", [(2 ** 22 + 77, 8), (2 ** 20 + 5, 520)])
+def test_norm_of_more_rows_than_workgroups(rows, n):
+    """A launch has at most 2^20 workgroups (of four rows, where rows are
+    short): the last rows are a workgroup's second."""
+    x, r, gamma = fill(rows, n), fill(rows, n), fill(n)
+    pick = sample(rows)
+    say("rmsnorm of many rows", rows, n)
+    y, h = gg.rmsnorm(x, gamma, residual=r)
+    want, hw = ref.rmsnorm(x[pick], r[pick], gamma, 1e-6)
+    ref.close(y[pick], want, want.abs() * 2.0 ** -8 + ref.rmsnorm_slack(want, n), "y")
+    ref.close(h[pick], hw, hw.abs() * (2.0 ** -8 + 2.0 ** -24), "h")
+    dx, _ = gg.rmsnorm_grad(y, h, gamma)
+    want, slack, _, _ = ref.rmsnorm_grad(y[pick], h[pick], gamma, None, 1e-6)
+    ref.close(dx[pick], want, want.abs() * 2.0 ** -8 + slack, "dx")
+
+
+def test_combine_gradient_of_more_tokens_than_workgroups():
+    dev = device()
+    tokens, n, e = 2 ** 20 + 33, 8, 7
+    expert = torch.randint(0, e, (tokens, 1), device=dev, dtype=torch.int32)
+    offs, row_slot, slot_row = gg.route(expert, e)
+    dout, y = fill(tokens, n), fill(row_slot.shape[0], n)
+    w = torch.rand(tokens, 1, device=dev)
+    say("combine_rows_grad of many tokens")
+    dy, dw = gg.combine_rows_grad(dout, y, slot_row, row_slot, offs, 1, weights=w)
+    slot = row_slot[:tokens].long()
+    assert int(offs[-1]) == tokens
+    assert torch.equal(dy[:tokens], (dout[slot].float() * w[slot]).to(BF))
+    part = y[slot_row.long()].double() * dout.double()
+    want = part.sum(-1).cpu()[:, None]
+    ref.close(dw, want, want.abs() * 2.0 ** -24 + part.abs().sum(-1).cpu()[:, None] * n * ref.U32, "dw")
 
 
 def test_silu_rows_over_4gb():
