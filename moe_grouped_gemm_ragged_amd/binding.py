@@ -982,9 +982,8 @@ def _grouped(t, name, dtype, groups, masked):
     return tuple(t.shape[:-1]), t.shape[-2], t.shape[-1]
 
 
-def _silu_mul_rows(h, groups, masked, keep, a, a8, a8s, kept, kept_scales):
+def _silu_mul_rows(h, lead, m, n, groups, masked, keep, a, a8, a8s, kept, kept_scales):
     torch = _torch()
-    lead, m, n = _grouped(h, "h", torch.bfloat16, groups, masked)
     if keep or kept is not None or kept_scales is not None:
         if n % 256:
             raise ValueError("e4m3 rows need I = n / 2 a multiple of 128")
@@ -1001,10 +1000,11 @@ def silu_mul_rows(h, groups, masked=False, keep=False, out=None, kept=None, kept
     ``keep`` (or a buffer for it) also writes h as e4m3 rows for
     ``fp8_silu_mul_grad``: returns (a, kept, kept_scales) then, else a."""
     torch = _torch()
-    if h.shape[-1] % 16:
+    lead, m, n = _grouped(h, "h", torch.bfloat16, groups, masked)
+    if n % 16:
         raise ValueError("h must have 2 I columns with I a multiple of 8")
-    a = _shaped(out, "out", torch.bfloat16, (*h.shape[:-1], h.shape[-1] // 2), h.device)
-    kept = _silu_mul_rows(h, groups, masked, keep, a, None, None, kept, kept_scales)
+    a = _shaped(out, "out", torch.bfloat16, (*lead, n // 2), h.device)
+    kept = _silu_mul_rows(h, lead, m, n, groups, masked, keep, a, None, None, kept, kept_scales)
     return (a, *kept) if kept else a
 
 
@@ -1012,12 +1012,13 @@ def fp8_silu_mul_rows(h, groups, masked=False, keep=False, out=None, out_scales=
     """silu_mul_rows with a as e4m3 rows (I a multiple of 128): returns (codes,
     scales) or (codes, scales, kept, kept_scales)."""
     torch = _torch()
-    if h.shape[-1] % 256:
+    lead, m, n = _grouped(h, "h", torch.bfloat16, groups, masked)
+    if n % 256:
         raise ValueError("e4m3 rows need I = n / 2 a multiple of 128")
-    lead, i = tuple(h.shape[:-1]), h.shape[-1] // 2
+    i = n // 2
     a8 = _shaped(out, "out", torch.uint8, (*lead, i), h.device)
     a8s = _shaped(out_scales, "out_scales", torch.uint8, (*lead, i // 128), h.device)
-    return (a8, a8s, *_silu_mul_rows(h, groups, masked, keep, None, a8, a8s, kept, kept_scales))
+    return (a8, a8s, *_silu_mul_rows(h, lead, m, n, groups, masked, keep, None, a8, a8s, kept, kept_scales))
 
 
 def _silu_mul_grad(da, h, h_scales, groups, masked, with_act, out, act):

@@ -195,3 +195,13 @@ def test_fp8_wgrad_checks_arguments(lib, name, case, status):
 def test_fp8_wgrad_binding_refuses(error, call):
     with pytest.raises(error):
         call()
+
+
+@pytest.mark.parametrize("f", [gg.silu_mul_rows, gg.fp8_silu_mul_rows])
+@pytest.mark.parametrize("shape", [(256,), (4, 4, 256), (4, 4, 4, 256)])
+@pytest.mark.parametrize("masked", [False, True])
+def test_silu_rows_binding_refuses_other_ranks(f, shape, masked):
+    if masked and len(shape) == 3:
+        shape = (3, *shape[1:])                # (a rank that is taken, with experts that do not match)
+    with pytest.raises(ValueError):
+        f(bf(*shape), I, masked=masked)
