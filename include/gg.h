@@ -571,7 +571,8 @@ gg_status gg_fp8_masked_wgrad(const void* x, const void* x_scales,
  * the block's finite values, and an infinity or NaN becomes the NaN code.
  * gg_fp8_pack_scales takes these scales (src_is_f32 = 0, ld_src = n / 128).
  * Rounding: a value of a block is off by at most 2^-4 of itself, or 2^-10 s
- * where it is below 2^-6 s.
+ * where it is below 2^-6 s.  (From 2^128 - 2^123 on a value becomes 2^128,
+ * which bf16 and fp32 do not hold; gg_silu_mul_grad takes it as it is.)
  *
  * gg_rmsnorm -- the norm in front of the layer, with the residual's addition:
  *   h = x + residual,  y = h / sqrt(mean(h^2) + eps) * gamma     for each row

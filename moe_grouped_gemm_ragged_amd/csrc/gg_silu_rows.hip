@@ -114,6 +114,9 @@ __global__ __launch_bounds__(kThreads) void silu_mul_grad_kernel(const uint16_t*
                                                                  const uint8_t* h_scales, const int32_t* groups,
                                                                  int32_t E, int64_t m, int64_t rows, int64_t width,
                                                                  uint16_t* dh, uint16_t* act) {
+  // g and u of kept rows are carried halved: a value from 2^128 - 2^123 on is
+  // kept as 2^128, which fp32 does not hold
+  constexpr float kUnit = H8 ? 0.5f : 1.0f, kUnits = 1.0f / kUnit;
   const int64_t end = MASKED ? rows : owned_rows(groups, E, rows);
   const int64_t kb = width / kBlock;
   for (Walk w((int)(width / 8)); w.row < end; w.next()) {
@@ -125,8 +128,8 @@ __global__ __launch_bounds__(kThreads) void silu_mul_grad_kernel(const uint16_t*
     if constexpr (H8) {
       const uint8_t* p = static_cast<const uint8_t*>(h) + at;
       const uint8_t* s = h_scales + w.row * 2 * kb + w.group / 16;
-      dequantise8(*reinterpret_cast<const u32x2r*>(p), scale_value(s[0]), g);
-      dequantise8(*reinterpret_cast<const u32x2r*>(p + width), scale_value(s[kb]), u);
+      dequantise8(*reinterpret_cast<const u32x2r*>(p), scale_value(s[0]) * kUnit, g);
+      dequantise8(*reinterpret_cast<const u32x2r*>(p + width), scale_value(s[kb]) * kUnit, u);
     } else {
       const uint16_t* p = static_cast<const uint16_t*>(h) + at;
       unpack8(load16(p), g);
@@ -135,11 +138,12 @@ __global__ __launch_bounds__(kThreads) void silu_mul_grad_kernel(const uint16_t*
     float dg[8], du[8], a[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const float s = sigmoid(g[e]);
+      const float s = sigmoid(g[e] * kUnits);
       const float gs = g[e] * s;
-      a[e] = gs * u[e];
-      du[e] = d[e] * gs;
-      dg[e] = d[e] * u[e] * s * (1.0f + g[e] * (1.0f - s));
+      a[e] = gs * u[e] * (kUnits * kUnits);
+      du[e] = d[e] * gs * kUnits;
+      // (g s, not g, times 1 - s: g may be infinite where s is 0)
+      dg[e] = d[e] * u[e] * (s + gs * (1.0f - s) * kUnits) * kUnits;
     }
     store16(dh + at, pack8(dg));
     store16(dh + at + width, pack8(du));
