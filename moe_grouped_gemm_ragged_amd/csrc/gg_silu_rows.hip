@@ -71,6 +71,16 @@ __device__ __forceinline__ bool owned(const int32_t* groups, int64_t m, int64_t 
 
 __device__ __forceinline__ float sigmoid(float g) { return __builtin_amdgcn_rcpf(1.0f + __expf(-g)); }
 
+// d u f for |f| < 1.1 (silu's derivative), where d u alone may leave fp32
+// although the product does not: the larger of d and u takes f first, so that
+// nothing underflows before its time, and f is halved on the way, so that
+// nothing overflows either (both exact).  65536 rows, I 768: 92.8 us from kept
+// rows, 92.2 with d u f from left to right, 109.1 and 110.1 from bf16 rows.
+__device__ __forceinline__ float product(float d, float u, float f) {
+  const bool first = fabsf(d) > fabsf(u);
+  return (first ? d : u) * (0.5f * f) * (first ? u : d) * 2.0f;
+}
+
 struct SiluOut {
   uint16_t* a;        // each pair may be null
   uint8_t* a8;
@@ -143,7 +153,7 @@ __global__ __launch_bounds__(kThreads) void silu_mul_grad_kernel(const uint16_t*
       a[e] = gs * u[e] * (kUnits * kUnits);
       du[e] = d[e] * gs * kUnits;
       // (g s, not g, times 1 - s: g may be infinite where s is 0)
-      dg[e] = d[e] * u[e] * (s + gs * (1.0f - s) * kUnits) * kUnits;
+      dg[e] = product(d[e], u[e], s + gs * (1.0f - s) * kUnits) * kUnits;
     }
     store16(dh + at, pack8(dg));
     store16(dh + at + width, pack8(du));
