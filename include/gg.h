@@ -540,10 +540,11 @@ gg_status gg_fp8_masked_forward(const void* x, const void* x_scales,
  *   x_scales  packed (GG_FP8_ACT_RAGGED, same offs)
  *   dy        [m, n]     bf16
  *   dw        [E, k, n]  dw_dtype, as gg_wgrad_ex
- * Xhat enters the matrix instructions as bf16, which holds it exactly while
- * its scale is at least 2^-117; otherwise as gg_wgrad_ex.  A scale byte of 0
- * counts as 0 here.  Without rows (m or max_m 0) x, x_scales and dy may be
- * NULL.
+ * Xhat enters the matrix instructions rounded to bf16, which holds it exactly
+ * for scales from 2^-124 to 2^119 (below, the smallest codes lose bits; above,
+ * the largest become infinities); otherwise as gg_wgrad_ex.  A scale byte b
+ * stands for 2^(b - 127), also where b is 0, and 255 for NaN, as in
+ * gg_fp8_forward.  Without rows (m or max_m 0) x, x_scales and dy may be NULL.
  * gg_fp8_masked_wgrad -- the same on the masked layout: x [E, max_m, k],
  * x_scales packed with GG_FP8_ACT_MASKED and the same masked_m.
  * Cited passages: sglang PR #32385, "Cause" (the fp8 operands and their

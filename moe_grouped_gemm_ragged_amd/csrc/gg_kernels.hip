@@ -609,7 +609,8 @@ __device__ __forceinline__ void x8_scales(const uint8_t* sa, int64_t tile_bytes,
 }
 
 // Converts a stage and writes it to its A region; byte: the stage's byte of
-// the scale dwords.
+// the scale dwords.  The conversion takes the scale's exponent bits alone, as
+// an E8M0 byte: 0 is 2^-127, 255 is NaN.
 __device__ __forceinline__ void x8_write(const u32x2 (&r)[4], const uint32_t (&sc)[4], int byte, int lane_in, int w,
                                          uint8_t* lds_op) {
   const int lane = (int)opaque_v((uint32_t)lane_in);

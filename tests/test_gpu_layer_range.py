@@ -72,3 +72,62 @@ def test_silu_mul_grad_of_kept_rows_beyond_fp32():
         beyond = want.abs() >= 2.0 ** 128
         assert torch.equal(got[beyond], want[beyond].sign() * float("inf")), what
         ref.close(got[~beyond], want[~beyond], room[~beyond], what)
+
+
+@pytest.mark.parametrize("masked", [False, True])
+@pytest.mark.parametrize("dtype", [torch.float32, BF])
+def test_fp8_wgrad_of_every_scale_byte(masked, dtype):
+    """One row an expert, all 256 codes under each of the 256 scale bytes, and
+    dY 1: dW is the row itself, rounded to bf16 as it enters."""
+    dev = device()
+    e = 256
+    codes = torch.arange(256, device=dev).to(torch.uint8).expand(e, 256).contiguous()
+    scales = torch.arange(e, device=dev).to(torch.uint8)[:, None].expand(e, 2).contiguous()
+    dy = torch.ones(e, 8, dtype=BF, device=dev)
+    c = codes.cpu().view(torch.float8_e4m3fn).double()
+    b = torch.arange(e, dtype=torch.float64)[:, None]
+    want = c * torch.where(b == 255, torch.full_like(b, float("nan")), torch.pow(2.0, b - 127))
+    exact = (b >= 3) & (b <= 246) & ~torch.isnan(c)
+    assert torch.equal(want.to(BF).double()[exact], want[exact])
+    if masked:
+        groups = torch.ones(e, dtype=torch.int32, device=dev)
+        packed = gg.fp8_pack_scales(gg.GG_FP8_ACT_MASKED, scales, groups, 1, 256, e)
+        say("fp8_masked_wgrad of every scale byte", dtype)
+        dw = gg.fp8_masked_wgrad(codes[:, None], packed, dy[:, None], groups, out_dtype=dtype)
+    else:
+        groups = torch.arange(1, e + 1, dtype=torch.int32, device=dev)
+        packed = gg.fp8_pack_scales(gg.GG_FP8_ACT_RAGGED, scales, groups, e, 256, e)
+        say("fp8_wgrad of every scale byte", dtype)
+        dw = gg.fp8_wgrad(codes, packed, dy, groups, out_dtype=dtype)
+    torch.cuda.synchronize()
+    got, want = ref.f64(dw), want.to(BF).double()[..., None].expand(e, 256, 8)
+    assert torch.equal(torch.isnan(got), torch.isnan(want))
+    there = ~torch.isnan(want)
+    assert torch.equal(got[there], want[there])
+
+
+def test_silu_mul_grad_of_every_scale_byte():
+    """Kept rows under scale bytes from 0 (2^-127) to 247 (448 2^120 leaves
+    bf16), and 255, NaN."""
+    dev = device()
+    b = torch.tensor([*range(248), 255])
+    rows = b.numel()
+    codes = torch.arange(128).to(torch.uint8).repeat(rows, 2)
+    codes[:, 127] = codes[:, 255] = 0x08                  # (no NaN codes)
+    scales = b.to(torch.uint8)[:, None].repeat(1, 2)
+    scales[:, 1] = 127
+    hv = ref.value(codes, scales)
+    hv[-1, :128] = float("nan")
+    da = torch.full((rows, 128), 2.0 ** 100, dtype=BF)
+    say("silu_mul_grad of every scale byte")
+    dh = gg.fp8_silu_mul_grad(da.to(dev), codes.to(dev), scales.to(dev),
+                              torch.tensor([rows], dtype=torch.int32, device=dev))
+    torch.cuda.synchronize()
+    want, slack = ref.silu_mul_grad(ref.f64(da), hv)
+    got = ref.f64(dh)
+    # (products of 2^100 and a code's 4 bits, the sigmoid being 1 at such gates: below 2^128 by a bf16
+    # step or more, or not at all)
+    beyond = want.abs() >= 2.0 ** 128
+    assert torch.equal(got[beyond], want[beyond].sign() * float("inf"))
+    want, slack = want.masked_fill(beyond, 0.0), slack.masked_fill(beyond, 0.0)
+    ref.close(got.masked_fill(beyond, 0.0), want, want.abs() * 2.0 ** -8 + slack, "dh")
