@@ -1,4 +1,5 @@
-"""GPU tests of the layer steps at the ends of the number range."""
+"""GPU tests of the layer steps at the ends of the number range, and of the
+norm gradient's longest sums against exact whole numbers."""
 import pytest
 import torch
 
@@ -131,3 +132,36 @@ def test_silu_mul_grad_of_every_scale_byte():
     assert torch.equal(got[beyond], want[beyond].sign() * float("inf"))
     want, slack = want.masked_fill(beyond, 0.0), slack.masked_fill(beyond, 0.0)
     ref.close(got.masked_fill(beyond, 0.0), want, want.abs() * 2.0 ** -8 + slack, "dh")
+
+
+@pytest.mark.parametrize("rows,n", [(2 ** 31 // 8192 + 300, 8192), (2 ** 22 + 77, 8), (2 ** 20 + 5, 512), (4099, 32768),
+                                    (1025, 64), (77, 1024)])
+def test_dgamma_of_many_rows_is_exact(rows, n):
+    """h of +-1 with eps 0 has rho 1 (n a power of two), so dgamma is the sum
+    of dy h: whole numbers from 1 to 3 whose sums stay below 2^24, exact in
+    fp32 in whatever order.  A row, a workgroup's share or a slice that is
+    lost, repeated or added to another column shows."""
+    dev = device()
+    i = torch.arange(rows, device=dev, dtype=torch.int32)
+    j = torch.arange(n, device=dev, dtype=torch.int32)
+    h, dy = torch.empty(rows, n, dtype=BF, device=dev), torch.empty(rows, n, dtype=BF, device=dev)
+    want = torch.zeros(n, dtype=torch.int64, device=dev)
+    step = max(1, 2 ** 27 // n)
+    for first in range(0, rows, step):
+        r = i[first:first + step, None]
+        sign = 1 - 2 * ((r * 5 + j * 3 + r // 7) % 2)
+        term = (r * 7 + j + r // 11) % 3 + 1
+        h[first:first + step] = sign.to(BF)
+        dy[first:first + step] = (term * sign).to(BF)
+        want += term.sum(0, dtype=torch.int64)
+    assert int(want.max()) < 2 ** 24
+    gamma = (j % 5 + 1).to(BF)
+    say("dgamma of many rows", rows, n)
+    dx, dgamma = gg.rmsnorm_grad(dy, h, gamma, eps=0.0)
+    torch.cuda.synchronize()
+    assert torch.equal(dgamma.double(), want.double())
+    # dx = p - u mean(p u), the mean of whole numbers from 1 to 15 summed exactly: one product, one
+    # difference and half a bf16 step
+    pick = torch.cat([torch.arange(min(rows, 8)), torch.arange(max(rows - 8, 0), rows)]).to(dev)
+    wx, _, _, _ = ref.rmsnorm_grad(dy[pick], h[pick], gamma, None, 0.0)
+    ref.close(dx[pick], wx, wx.abs() * 2.0 ** -8 + 15 * 4 * ref.U32, "dx")
