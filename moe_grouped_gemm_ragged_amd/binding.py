@@ -870,10 +870,12 @@ def rmsnorm(x, gamma, residual=None, eps=1e-6, out=None, h_out=None):
     return y, h
 
 
-def fp8_rmsnorm(x, gamma, residual=None, eps=1e-6, out=None, out_scales=None, h_out=None, with_bf16=False):
+def fp8_rmsnorm(x, gamma, residual=None, eps=1e-6, out=None, out_scales=None, h_out=None, with_bf16=False,
+                y_out=None):
     """rmsnorm with y as e4m3 rows: uint8 codes [rows, n] and E8M0 bytes
     [rows, n / 128] (n a multiple of 128).  Returns (codes, scales, h), or
-    (codes, scales, h, y) with the bf16 y too (``with_bf16``)."""
+    (codes, scales, h, y) with the bf16 y too (``with_bf16``, or a buffer for
+    it)."""
     torch = _torch()
     dev = x.device
     _check(x, "x", torch.bfloat16, 2, dev)
@@ -882,9 +884,11 @@ def fp8_rmsnorm(x, gamma, residual=None, eps=1e-6, out=None, out_scales=None, h_
         raise ValueError("x must be [rows, n] with n a multiple of 128")
     y8 = _shaped(out, "out", torch.uint8, (rows, n), dev)
     scales = _shaped(out_scales, "out_scales", torch.uint8, (rows, n // 128), dev)
-    y = torch.empty_like(x) if with_bf16 else None
+    y = None
+    if with_bf16 or y_out is not None:
+        y = _shaped(y_out, "y_out", torch.bfloat16, x.shape, dev, like=x)
     h = _rmsnorm(x, gamma, residual, eps, y, y8, scales, h_out)
-    return (y8, scales, h, y) if with_bf16 else (y8, scales, h)
+    return (y8, scales, h) if y is None else (y8, scales, h, y)
 
 
 def rmsnorm_grad_workspace_bytes(rows, n) -> int:
@@ -941,7 +945,8 @@ def fp8_gather_rows(src, scales, row_slot, topk, offs, out=None, out_scales=None
     return out, out_scales
 
 
-def combine_rows_grad(dout, y, slot_row, row_slot, offs, topk, weights=None, out=None, with_weights=True):
+def combine_rows_grad(dout, y, slot_row, row_slot, offs, topk, weights=None, out=None, with_weights=True,
+                      dweights=None):
     """Gradient of combine_rows (gg_combine_rows_grad): dout bf16 or fp32
     [tokens, n], y bf16 [rows, n] (None without ``with_weights``), and the
     routing.  Returns (dy bf16 [len(row_slot), n], dweights fp32 [tokens,
@@ -964,7 +969,9 @@ def combine_rows_grad(dout, y, slot_row, row_slot, offs, topk, weights=None, out
         if y is None:
             raise ValueError("the gradient of the weights needs y")
         _shaped(y, "y", torch.bfloat16, (cap, n), dev)
-        dw = _shaped(None, "dweights", torch.float32, (tokens, topk), dev)
+        dw = _shaped(dweights, "dweights", torch.float32, (tokens, topk), dev)
+    elif dweights is not None:
+        raise ValueError("dweights without with_weights")
     out = _shaped(out, "out", torch.bfloat16, (cap, n), dev)
     _launch("gg_combine_rows_grad", dev, _ptr(dout), _dtype_code(dout.dtype), _ptr(y) if with_weights else None, n,
             _ptr(slot_row), _ptr(row_slot), _ptr(offs), e, _ptr(weights), topk, tokens, cap, _ptr(out), _ptr(dw))
