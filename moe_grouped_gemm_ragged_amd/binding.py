@@ -184,23 +184,38 @@ def _check(t, name, dtype, ndim, device):
         raise ValueError(f"{name} must be contiguous")
 
 
-def _stream_handle(device) -> int:
+def _launch(name, dev, *args):
+    """Calls an entry point on ``dev``'s current stream, with ``dev`` current
+    (a kernel goes to the current device)."""
     torch = _torch()
-    return int(torch.cuda.current_stream(device).cuda_stream)
+    if dev.type != "cuda":
+        raise ValueError(f"{name}: the tensors are on {dev}, expected a GPU")
+    f = getattr(load(), name)
+    if torch.cuda.current_device() == dev.index:
+        rc = f(*args, _raw_stream(dev.index))
+    else:
+        with torch.cuda.device(dev):
+            rc = f(*args, _raw_stream(dev.index))
+    if rc != 0:
+        raise GGError(name, rc, last_error())
+
+
+def _raw_stream(index):
+    """The current stream's handle without a Stream object around it (2 us of
+    a small call's 10), where this torch has that."""
+    torch = _torch()
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return raw(index) if raw is not None else int(torch.cuda.current_stream(index).cuda_stream)
 
 
 def _invoke(name, a, b, groups, out, out_code, m, k, n, e, device, alpha=1.0, beta=0.0):
     """Calls the plain entry point, or its *_ex form when alpha != 1 or
     beta != 0."""
+    ptrs = a.data_ptr(), b.data_ptr(), groups.data_ptr(), out.data_ptr()
     if float(alpha) == 1.0 and float(beta) == 0.0:
-        rc = call_raw(name, a.data_ptr(), b.data_ptr(), groups.data_ptr(), out.data_ptr(), out_code,
-                      int(m), int(k), int(n), int(e), _stream_handle(device))
+        _launch(name, device, *ptrs, out_code, int(m), int(k), int(n), int(e))
     else:
-        name = name + "_ex"
-        rc = call_raw(name, a.data_ptr(), b.data_ptr(), groups.data_ptr(), out.data_ptr(), out_code,
-                      int(m), int(k), int(n), int(e), float(alpha), float(beta), _stream_handle(device))
-    if rc != 0:
-        raise GGError(name, rc, last_error())
+        _launch(name + "_ex", device, *ptrs, out_code, int(m), int(k), int(n), int(e), float(alpha), float(beta))
 
 
 def _need_out(out, beta):
@@ -398,11 +413,6 @@ def masked_forward_silu_mul(x, w13, masked_m, out=None, out_dtype=None):
 # producing the grouped layout
 # ---------------------------------------------------------------------------
 
-def _raise(name, rc):
-    if rc != 0:
-        raise GGError(name, rc, last_error())
-
-
 def offsets_from_splits(m_splits, min_alignment=1, pad_empty=False, out=None):
     """int32 end offsets from int64 per-expert row counts on the device
     (gg_offsets_from_splits), each count padded to min_alignment."""
@@ -413,9 +423,8 @@ def offsets_from_splits(m_splits, min_alignment=1, pad_empty=False, out=None):
     if out is None:
         out = torch.empty(e, dtype=torch.int32, device=dev)
     _check(out, "out", torch.int32, 1, dev)
-    _raise("gg_offsets_from_splits", call_raw("gg_offsets_from_splits", m_splits.data_ptr(), int(e),
-                                              int(min_alignment), 1 if pad_empty else 0, out.data_ptr(),
-                                              _stream_handle(dev)))
+    _launch("gg_offsets_from_splits", dev, m_splits.data_ptr(), int(e), int(min_alignment), 1 if pad_empty else 0,
+            out.data_ptr())
     return out
 
 
@@ -441,10 +450,8 @@ def route(expert_of_slot, num_groups, min_alignment=1, pad_empty=False, rows_cap
     row_slot = torch.empty(max(cap, 1), dtype=torch.int32, device=dev)
     slot_row = torch.empty(max(slots, 1), dtype=torch.int32, device=dev)
     ws = torch.empty(int(load().gg_route_workspace_bytes(slots, num_groups)), dtype=torch.uint8, device=dev)
-    _raise("gg_route", call_raw("gg_route", expert_of_slot.data_ptr(), int(slots), int(num_groups),
-                                int(min_alignment), 1 if pad_empty else 0, offs.data_ptr(),
-                                row_slot.data_ptr(), int(cap), slot_row.data_ptr(), ws.data_ptr(),
-                                _stream_handle(dev)))
+    _launch("gg_route", dev, expert_of_slot.data_ptr(), int(slots), int(num_groups), int(min_alignment),
+            1 if pad_empty else 0, offs.data_ptr(), row_slot.data_ptr(), int(cap), slot_row.data_ptr(), ws.data_ptr())
     return offs, row_slot[:cap], slot_row[:slots]
 
 
@@ -460,9 +467,8 @@ def gather_rows(src, row_slot, topk, offs, out=None):
     rows_cap = row_slot.shape[0]
     if out is None:
         out = torch.empty((rows_cap, *src.shape[1:]), dtype=src.dtype, device=dev)
-    _raise("gg_gather_rows", call_raw("gg_gather_rows", src.data_ptr(), int(tokens), int(row_bytes),
-                                      row_slot.data_ptr(), int(topk), offs.data_ptr(), int(offs.shape[0]),
-                                      int(rows_cap), out.data_ptr(), _stream_handle(dev)))
+    _launch("gg_gather_rows", dev, src.data_ptr(), int(tokens), int(row_bytes), row_slot.data_ptr(), int(topk),
+            offs.data_ptr(), int(offs.shape[0]), int(rows_cap), out.data_ptr())
     return out
 
 
@@ -477,10 +483,9 @@ def combine_rows(y, slot_row, topk, weights=None, out=None, out_dtype=None):
     tokens = slots // topk
     if out is None:
         out = torch.empty((tokens, n), dtype=out_dtype or torch.bfloat16, device=dev)
-    _raise("gg_combine_rows", call_raw("gg_combine_rows", y.data_ptr(), int(n), slot_row.data_ptr(),
-                                       None if weights is None else weights.data_ptr(), int(topk),
-                                       int(tokens), int(rows_cap), out.data_ptr(), _dtype_code(out.dtype),
-                                       _stream_handle(dev)))
+    _launch("gg_combine_rows", dev, y.data_ptr(), int(n), slot_row.data_ptr(),
+            None if weights is None else weights.data_ptr(), int(topk), int(tokens), int(rows_cap), out.data_ptr(),
+            _dtype_code(out.dtype))
     return out
 
 
@@ -496,12 +501,9 @@ def _bias_call(name, x, w, groups, bias, bias_scale, out, m, k, n, e, dev, alpha
     if bias_scale is not None:
         if bias_scale.dtype != torch.float32 or bias_scale.device != dev or not bias_scale.is_contiguous():
             raise TypeError("bias_scale must be a contiguous float32 tensor on the device")
-    rc = call_raw(name, x.data_ptr(), w.data_ptr(), groups.data_ptr(), bias.data_ptr(),
-                  None if bias_scale is None else bias_scale.data_ptr(), out.data_ptr(),
-                  _dtype_code(out.dtype), int(m), int(k), int(n), int(e), float(alpha), float(beta),
-                  _stream_handle(dev))
-    if rc != 0:
-        raise GGError(name, rc, last_error())
+    _launch(name, dev, x.data_ptr(), w.data_ptr(), groups.data_ptr(), bias.data_ptr(),
+            None if bias_scale is None else bias_scale.data_ptr(), out.data_ptr(), _dtype_code(out.dtype), int(m),
+            int(k), int(n), int(e), float(alpha), float(beta))
 
 
 def forward_bias(x, w, offs, bias, bias_scale=None, out=None, out_dtype=None, alpha=1.0, beta=0.0):
@@ -564,9 +566,8 @@ def bias_grad(dy, groups, bias_scale=None, masked=False, out=None):
         out = torch.empty((e, n), dtype=torch.float32, device=dev)
     _check(out, "out", torch.float32, 2, dev)
     name = "gg_masked_bias_grad" if masked else "gg_bias_grad"
-    _raise(name, call_raw(name, dy.data_ptr(), groups.data_ptr(),
-                          None if bias_scale is None else bias_scale.data_ptr(), out.data_ptr(), int(rows),
-                          int(n), int(e), _stream_handle(dev)))
+    _launch(name, dev, dy.data_ptr(), groups.data_ptr(), None if bias_scale is None else bias_scale.data_ptr(),
+            out.data_ptr(), int(rows), int(n), int(e))
     return out
 
 
@@ -586,8 +587,7 @@ def bias_scale_grad(dy, groups, bias, masked=False, out=None):
         out = torch.full((total,), float("nan"), dtype=torch.float32, device=dev)
     _check(out, "out", torch.float32, 1, dev)
     name = "gg_masked_bias_scale_grad" if masked else "gg_bias_scale_grad"
-    _raise(name, call_raw(name, dy.data_ptr(), groups.data_ptr(), bias.data_ptr(), out.data_ptr(), int(rows),
-                          int(n), int(e), _stream_handle(dev)))
+    _launch(name, dev, dy.data_ptr(), groups.data_ptr(), bias.data_ptr(), out.data_ptr(), int(rows), int(n), int(e))
     return out
 
 
@@ -722,22 +722,15 @@ def fp8_pack_scales(layout: int, scales, groups, rows: int, k: int, num_groups: 
         raise ValueError(f"out must hold {nbytes} bytes")
     if bad_count is not None:
         _check(bad_count, "bad_count", torch.int32, 1, dev)
-    rc = call_raw("gg_fp8_pack_scales", int(layout), scales.data_ptr(),
-                  1 if scales.dtype == torch.float32 else 0, int(scales.shape[-1]),
-                  None if groups is None else groups.data_ptr(), int(rows), int(k), int(num_groups),
-                  out.data_ptr(), None if bad_count is None else bad_count.data_ptr(),
-                  _stream_handle(dev))
-    if rc != 0:
-        raise GGError("gg_fp8_pack_scales", rc, last_error())
+    _launch("gg_fp8_pack_scales", dev, int(layout), scales.data_ptr(), 1 if scales.dtype == torch.float32 else 0,
+            int(scales.shape[-1]), None if groups is None else groups.data_ptr(), int(rows), int(k), int(num_groups),
+            out.data_ptr(), None if bad_count is None else bad_count.data_ptr())
     return out
 
 
 def _fp8_call(name, x, xs, w, ws, groups, out, m, k, n, e, dev):
-    rc = call_raw(name, x.data_ptr(), xs.data_ptr(), w.data_ptr(), ws.data_ptr(), groups.data_ptr(),
-                  out.data_ptr(), _dtype_code(out.dtype), int(m), int(k), int(n), int(e),
-                  _stream_handle(dev))
-    if rc != 0:
-        raise GGError(name, rc, last_error())
+    _launch(name, dev, x.data_ptr(), xs.data_ptr(), w.data_ptr(), ws.data_ptr(), groups.data_ptr(), out.data_ptr(),
+            _dtype_code(out.dtype), int(m), int(k), int(n), int(e))
 
 
 def fp8_forward(x, x_scales, w, w_scales, offs, out=None, out_dtype=None):
@@ -797,30 +790,6 @@ def fp8_masked_forward(x, x_scales, w, w_scales, masked_m, out=None, out_dtype=N
 # ---------------------------------------------------------------------------
 # norm, 8-bit gather, combine gradient, SiLU-mul rows
 # ---------------------------------------------------------------------------
-
-def _launch(name, dev, *args):
-    """Calls an entry point on ``dev``'s current stream, with ``dev`` current
-    (a kernel goes to the current device)."""
-    torch = _torch()
-    if dev.type != "cuda":
-        raise ValueError(f"{name}: the tensors are on {dev}, expected a GPU")
-    f = getattr(load(), name)
-    if torch.cuda.current_device() == dev.index:
-        rc = f(*args, _raw_stream(dev.index))
-    else:
-        with torch.cuda.device(dev):
-            rc = f(*args, _raw_stream(dev.index))
-    if rc != 0:
-        raise GGError(name, rc, last_error())
-
-
-def _raw_stream(index):
-    """The current stream's handle without a Stream object around it (2 us of
-    a small call's 10), where this torch has that."""
-    torch = _torch()
-    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    return raw(index) if raw is not None else int(torch.cuda.current_stream(index).cuda_stream)
-
 
 def _shaped(t, name, dtype, shape, device, like=None):
     """``t`` checked against a shape (of up to 3 dimensions), or a new tensor
