@@ -5,6 +5,7 @@
 #include <stdint.h>
 
 #include <atomic>
+#include <cfloat>
 #include <cstdio>
 #include <mutex>
 #include <string>
@@ -635,7 +636,7 @@ gg_status gg_fp8_masked_wgrad(const void* x, const void* x_scales, const void* d
 static gg_status norm_check(int64_t rows, int64_t n, float eps) {
   if (rows < 0 || rows >= kRowLimit || n < 8 || n % 8 != 0 || n > GG_MAX_KN)
     return fail(GG_ERR_BAD_DIM, "need 0 <= rows < 2^31 - 2^16 and n a positive multiple of 8 up to GG_MAX_KN");
-  if (!(eps >= 0.0f) || eps > 3.0e38f) return fail(GG_ERR_BAD_DIM, "eps must be a finite number >= 0");
+  if (!(eps >= 0.0f) || eps > FLT_MAX) return fail(GG_ERR_BAD_DIM, "eps must be a finite number >= 0");
   return GG_OK;
 }
 
