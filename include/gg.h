@@ -605,6 +605,8 @@ gg_status gg_fp8_masked_wgrad(const void* x, const void* x_scales,
  *                        device memory, 16-byte aligned, the caller's; its
  *                        contents on entry do not matter.  Calls that may
  *                        overlap need one each.
+ * A row's sums of h^2 and of p h are held in fp32: one that leaves its range
+ * gives a dx (and a share of dgamma) that is 0, inexact or not finite.
  *
  * gg_fp8_gather_rows -- gg_gather_rows for e4m3 rows with their scales, ready
  * for gg_fp8_forward on the same offs:
