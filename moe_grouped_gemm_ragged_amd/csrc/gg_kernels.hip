@@ -1486,8 +1486,8 @@ __device__ __forceinline__ void store_tile_lds(uint8_t* cbase, uint32_t ldc_byte
                    pack_bf16x2(hi[0], hi[1]), pack_bf16x2(hi[2], hi[3])};
         __builtin_amdgcn_raw_buffer_store_b128(o, rs, voff, 0, AUX);
       }
-      // one slab row group at a time (hoisting the prior-output loads of
-      // all four would need 32 more registers)
+      // one slab row group at a time (the prior output of all four at once
+      // would take 32 registers)
       if constexpr (SCALED) __builtin_amdgcn_sched_barrier(0);
     }
     // the next block row rewrites the slab: wait for this row's reads
@@ -1507,9 +1507,10 @@ __device__ __forceinline__ void store_tile_lds(uint8_t* cbase, uint32_t ldc_byte
 // again, while x and dY are shared by an expert's tiles.  128 experts of 128
 // rows, k 2048: n 1536 340 -> 300 us, but n 1000, whose lines the stores fill in
 // parts, 264 -> 349; 256 experts, k 7168, n 2048 2774 -> 2676; 512 rows and more
-// within 2 %.  bf16 dW (store_tile_lds) by the same rule: 128 rows, n 1536 252
-// -> 220 us, 64 masked experts of at most 256 rows, 768 x 2048 67 -> 64, 256
-// experts, k 7168, n 2048 2147 -> 2250; n 1032 390, 515 without the rule.
+// within 2 %.  bf16 dW (store_tile_lds) by the same rule: 128 rows, n 1536 235
+// -> 202 us, 64 masked experts of at most 256 rows, 768 x 2048 66 -> 64; n 1032,
+// k 4096, where the rule keeps plain stores, 378 against 519; but 256 experts,
+// k 7168, n 2048 2095 -> 2175, the one shape measured that loses by it.
 template <bool SCALED, bool NT>
 __device__ __forceinline__ void store_tile_x8(uint8_t* cbase, uint32_t ldc_bytes, int rows, int cols, int wm, int wn,
                                               int lane, const floatx16 (&acc)[TM][TN], uint8_t* slab, float alpha,

@@ -348,9 +348,10 @@ constexpr int64_t kMostBlocks = 1 << 20;   // a launch's threads stay below 2^32
 
 // Threads of a workgroup of the gradient, in slices of a row each, and the
 // most workgroups (workspace rows): one large workgroup a compute unit keeps
-// the workspace small and still has its waves' loads in flight.  8192 x 6144:
-// 82 us (4.9 TB/s) with 256 workgroups of 768, 86 with 512 of 512 or of a
-// single slice; 16384 x 512: 18.3 us, 34.9 with 512 of a single slice.
+// the workspace small and still has its waves' loads in flight.  Both kernels
+// together, 256 workgroups of 768 against 512 of 512 and 512 of a single slice:
+// 8192 x 6144 with dh 78.0, 78.3 and 78.1 us, 16384 x 512 14.8, 15.5 and 26.8,
+// 4096 x 2048 with dh 17.5, 16.0 and 18.9.
 constexpr int kGradThreads = 768;
 constexpr int kGradGroups = 256;
 int grad_slices(int threads) { return threads >= kGradThreads ? 1 : kGradThreads / threads; }

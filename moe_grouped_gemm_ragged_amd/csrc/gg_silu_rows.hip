@@ -7,6 +7,8 @@
 //   a = g s u
 //   dg = da u s (1 + g (1 - s)),   du = da g s
 //
+// in an order that stays in fp32 wherever the gradient does (see product).
+//
 // The forward step writes a (bf16, or e4m3 rows with one power-of-two scale
 // per 128 values: the fp8 down projection's operand) and can keep h in 8 bits
 // for the backward step: 2 I + I / 64 bytes a row instead of 4 I.  The
