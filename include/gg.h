@@ -697,6 +697,111 @@ gg_status gg_masked_silu_mul_grad(const void* da, const void* h,
                                   int64_t max_m, int64_t n,
                                   int32_t num_groups, void* stream);
 
+/*
+ * 4-bit rows and weights
+ * ----------------------
+ * The grouped product on microscaled 4-bit operands (OCP MX: e2m1 codes with
+ * one power-of-two scale per 32 values), and the steps that produce them.
+ *
+ * 4-bit rows: e2m1 codes (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives),
+ * two in a byte, value 2j of a row in the low half of byte j, so a row of k
+ * values takes k / 2 bytes; k is a multiple of 32.  Every 32 consecutive
+ * values share one E8M0 scale byte (2^(b - 127), 255 for NaN).
+ * The quantising calls take the smallest power of two s with amax / s <= 6, 1
+ * for a block of zeros, never below 2^-126, and round value / s to the nearest
+ * code, ties to the even one.  A block with an infinity or NaN gets the scale
+ * 255 and codes of 0, so all of it is NaN (e2m1 has neither).  Rounding: a value
+ * is off by at most 2^-2 of itself, or s / 4 where it is below s.  (From
+ * 0.875 * 2^128 on a value becomes 2^128, which bf16 does not hold.)
+ *
+ * Scales are consumed in a packed, tile-major layout: for every 256 rows of an
+ * operand (an expert's rows from its first one on; tiles counted as in the fp8
+ * layout) and every 128 values (a last stage may be partly filled) 1024 bytes
+ * at (tile * ceil(k / 128) + stage) * 1024, where block q (0..3) of tile row r
+ * lies at 512 (r / 128) + 16 (r mod 32) + 8 (q mod 2) + 4 (q / 2) + (r / 32) mod 4.
+ *
+ * Layouts of rows (groups / rows):
+ *   GG_FP4_ACT_RAGGED  [rows, k], groups = end offsets
+ *   GG_FP4_ACT_MASKED  [E, rows, k], groups = masked_m
+ *   GG_FP4_WEIGHT      [E, rows, k], rows = n, all of them; groups unused
+ * Rows that no expert owns are neither read nor written.
+ *
+ * gg_fp4_scale_bytes -- bytes of an operand's packed scales (ragged: an upper
+ *   bound, as gg_fp8_scale_bytes); -1 for invalid arguments.
+ * gg_fp4_pack_scales -- packed scales from E8M0 bytes, as a checkpoint holds
+ *   them: src[row * ld_src + block], ld_src >= k / 32.  Bytes of a tile's rows
+ *   that no expert owns become 0.
+ * gg_fp4_quantize -- x bf16 rows to codes (k / 2 bytes a row) and their packed
+ *   scales (gg_fp4_scale_bytes, 16-byte aligned; tiles without rows untouched).
+ * gg_fp4_gather_rows -- gg_gather_rows to 4-bit rows: codes and packed scales
+ *   (GG_FP4_ACT_RAGGED over rows_cap rows) of src[row_slot[r] / topk] for r
+ *   below the last end offset; zero codes and the scale 1 for a padding row.
+ *   src [tokens, k] bf16; row_slot and offs as gg_route wrote them.
+ * gg_fp4_silu_mul_rows, gg_fp4_masked_silu_mul_rows -- 4-bit rows of
+ *   a = silu(g) u (in fp32) from gate/up rows h bf16 [m, n], n = 2 I, gate
+ *   columns first; I a multiple of 32.
+ * gg_fp4_dequantize -- out = code * scale in bf16 [.., k] (exact).  Its uses:
+ *   the operands of a training step's gradients (gg_dgrad_nk, gg_wgrad_nk), and
+ *   4-bit weights for the bf16 passes.
+ * gg_fp4_forward -- Y[rows of g] = sum_k x sx w[g] sw:
+ *   x  [m, k / 2] bytes, x_scales packed (GG_FP4_ACT_RAGGED, same offs)
+ *   w  [E, n, k / 2] bytes, w_scales packed (GG_FP4_WEIGHT, rows = n)
+ *   y  [m, n] y_dtype; rows past end(E-1) untouched
+ *   Products of codes and scales are exact; each 64-deep scaled matrix
+ *   instruction's sum is added into an fp32 accumulator.  A scale of 255 gives
+ *   NaN in the rows (columns) it belongs to.
+ * gg_fp4_masked_forward -- the same on the masked layout.
+ *
+ * Requirements and errors: those of gg_forward, k (I) a multiple of 32,
+ * pointers 16-byte aligned but for src of gg_fp4_pack_scales and the int32
+ * arrays.  Without rows their pointers may be NULL.  All calls are
+ * deterministic, take no workspace and are safe to capture in a HIP graph.
+ * Cited passages: sglang PR #32385, "Cause" (power-of-two scales of blocks
+ * along the reduction, between the layer's steps); PyTorch issue #152668,
+ * "Describe the bug" (the permute step).
+ */
+typedef enum {
+    GG_FP4_ACT_RAGGED = 0,
+    GG_FP4_ACT_MASKED = 1,
+    GG_FP4_WEIGHT = 2
+} gg_fp4_layout;
+
+int64_t gg_fp4_scale_bytes(gg_fp4_layout layout, int64_t rows, int64_t k,
+                           int32_t num_groups);
+gg_status gg_fp4_pack_scales(gg_fp4_layout layout, const void* src,
+                             int64_t ld_src, const int32_t* groups,
+                             int64_t rows, int64_t k, int32_t num_groups,
+                             void* dst, void* stream);
+gg_status gg_fp4_quantize(gg_fp4_layout layout, const void* x,
+                          const int32_t* groups, int64_t rows, int64_t k,
+                          int32_t num_groups, void* codes, void* scales,
+                          void* stream);
+gg_status gg_fp4_gather_rows(const void* src, int64_t tokens, int64_t k,
+                             const int32_t* row_slot, int32_t topk,
+                             const int32_t* offs, int32_t num_groups,
+                             int64_t rows_cap, void* codes, void* scales,
+                             void* stream);
+gg_status gg_fp4_silu_mul_rows(const void* h, const int32_t* offs, void* codes,
+                               void* scales, int64_t m, int64_t n,
+                               int32_t num_groups, void* stream);
+gg_status gg_fp4_masked_silu_mul_rows(const void* h, const int32_t* masked_m,
+                                      void* codes, void* scales, int64_t max_m,
+                                      int64_t n, int32_t num_groups,
+                                      void* stream);
+gg_status gg_fp4_dequantize(gg_fp4_layout layout, const void* codes,
+                            const void* scales, const int32_t* groups,
+                            int64_t rows, int64_t k, int32_t num_groups,
+                            void* out, void* stream);
+gg_status gg_fp4_forward(const void* x, const void* x_scales, const void* w,
+                         const void* w_scales, const int32_t* offs, void* y,
+                         gg_dtype y_dtype, int64_t m, int64_t k, int64_t n,
+                         int32_t num_groups, void* stream);
+gg_status gg_fp4_masked_forward(const void* x, const void* x_scales,
+                                const void* w, const void* w_scales,
+                                const int32_t* masked_m, void* y,
+                                gg_dtype y_dtype, int64_t max_m, int64_t k,
+                                int64_t n, int32_t num_groups, void* stream);
+
 /* Static description of a status code. */
 const char* gg_status_str(gg_status s);
 

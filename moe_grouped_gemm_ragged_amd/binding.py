@@ -124,6 +124,18 @@ def load():
         getattr(lib, name).restype = ctypes.c_int
     lib.gg_rmsnorm_grad_workspace_bytes.argtypes = [I64, I64]
     lib.gg_rmsnorm_grad_workspace_bytes.restype = ctypes.c_int64
+    lib.gg_fp4_scale_bytes.argtypes = [ctypes.c_int, I64, I64, I32]
+    lib.gg_fp4_scale_bytes.restype = ctypes.c_int64
+    for name, args in (("gg_fp4_pack_scales", [ctypes.c_int, P, I64, P, I64, I64, I32, P, P]),
+                       ("gg_fp4_quantize", [ctypes.c_int, P, P, I64, I64, I32, P, P, P]),
+                       ("gg_fp4_gather_rows", [P, I64, I64, P, I32, P, I32, I64, P, P, P]),
+                       ("gg_fp4_silu_mul_rows", [P, P, P, P, I64, I64, I32, P]),
+                       ("gg_fp4_masked_silu_mul_rows", [P, P, P, P, I64, I64, I32, P]),
+                       ("gg_fp4_dequantize", [ctypes.c_int, P, P, P, I64, I64, I32, P, P]),
+                       ("gg_fp4_forward", [P, P, P, P, P, P, ctypes.c_int, I64, I64, I64, I32, P]),
+                       ("gg_fp4_masked_forward", [P, P, P, P, P, P, ctypes.c_int, I64, I64, I64, I32, P])):
+        getattr(lib, name).argtypes = args
+        getattr(lib, name).restype = ctypes.c_int
     lib.gg_status_str.argtypes = [ctypes.c_int]
     lib.gg_status_str.restype = ctypes.c_char_p
     lib.gg_last_error.argtypes = []
@@ -1065,3 +1077,161 @@ def fp8_masked_wgrad(x, x_scales, dy, masked_m, out=None, out_dtype=None, alpha=
     """fp8_wgrad on the masked layout: x uint8 [E, max_m, k], x_scales packed
     with GG_FP8_ACT_MASKED and the same masked_m; dy bf16 [E, max_m, n]."""
     return _fp8_wgrad("gg_fp8_masked_wgrad", GG_FP8_ACT_MASKED, x, x_scales, dy, masked_m, out, out_dtype, alpha, beta)
+
+
+# ---------------------------------------------------------------------------
+# 4-bit rows and weights
+# ---------------------------------------------------------------------------
+
+GG_FP4_ACT_RAGGED = 0
+GG_FP4_ACT_MASKED = 1
+GG_FP4_WEIGHT = 2
+
+
+def fp4_scale_bytes(layout: int, rows: int, k: int, num_groups: int) -> int:
+    """Bytes of packed scales (gg_fp4_scale_bytes)."""
+    v = int(load().gg_fp4_scale_bytes(int(layout), int(rows), int(k), int(num_groups)))
+    if v < 0:
+        raise ValueError("invalid arguments for gg_fp4_scale_bytes")
+    return v
+
+
+def _fp4_rows(layout, t, name, dtype, groups):
+    """Checks rows in one of the layouts; returns (their leading dimensions,
+    rows as the library counts them, width, experts)."""
+    if layout not in (GG_FP4_ACT_RAGGED, GG_FP4_ACT_MASKED, GG_FP4_WEIGHT):
+        raise ValueError(f"unknown layout {layout}")
+    ragged = layout == GG_FP4_ACT_RAGGED
+    _check(t, name, dtype, 2 if ragged else 3, t.device)
+    if layout == GG_FP4_WEIGHT:
+        if groups is not None:
+            raise ValueError("weights take no groups")
+        return tuple(t.shape[:2]), t.shape[1], t.shape[2], t.shape[0]
+    _check(groups, "groups", _torch().int32, 1, t.device)
+    if not ragged and t.shape[0] != groups.shape[0]:
+        raise ValueError(f"{name} and groups must have the same number of experts")
+    return tuple(t.shape[:-1]), t.shape[-2], t.shape[-1], groups.shape[0]
+
+
+def _packed4(scales, name, layout, rows, k, experts, device):
+    """Checks packed scales against the bytes they need, or makes them."""
+    torch = _torch()
+    need = fp4_scale_bytes(layout, rows, k, experts)
+    if scales is None:
+        return _shaped(None, name, torch.uint8, (need,), device)
+    _check(scales, name, torch.uint8, 1, device)
+    if scales.numel() < need:
+        raise ValueError(f"{name} must hold {need} bytes")
+    return scales
+
+
+def fp4_pack_scales(layout: int, scales, groups=None, out=None):
+    """Packed scales of one operand from E8M0 bytes (gg_fp4_pack_scales):
+    scales uint8 [m, k / 32] (ragged), [E, max_m, k / 32] or [E, n, k / 32];
+    groups: the int32 end offsets / masked_m (None for weights)."""
+    torch = _torch()
+    _, rows, blocks, e = _fp4_rows(layout, scales, "scales", torch.uint8, groups)
+    out = _packed4(out, "out", layout, rows, 32 * blocks, e, scales.device)
+    _launch("gg_fp4_pack_scales", scales.device, int(layout), _ptr(scales), blocks, _ptr(groups), rows, 32 * blocks, e,
+            _ptr(out))
+    return out
+
+
+def fp4_quantize(layout: int, x, groups=None, out=None, out_scales=None):
+    """4-bit rows of x (gg_fp4_quantize): bf16 [m, k], or [E, max_m, k] or
+    weights [E, n, k] by ``layout``, k a multiple of 32.  Returns (codes uint8
+    [..., k / 2], packed scales); rows no expert owns are left untouched."""
+    torch = _torch()
+    lead, rows, k, e = _fp4_rows(layout, x, "x", torch.bfloat16, groups)
+    if k % 32:
+        raise ValueError("x must have a multiple of 32 columns")
+    out = _shaped(out, "out", torch.uint8, (*lead, k // 2), x.device)
+    out_scales = _packed4(out_scales, "out_scales", layout, rows, k, e, x.device)
+    _launch("gg_fp4_quantize", x.device, int(layout), _ptr(x), _ptr(groups), rows, k, e, _ptr(out), _ptr(out_scales))
+    return out, out_scales
+
+
+def fp4_dequantize(layout: int, codes, scales, groups=None, out=None):
+    """bf16 values of 4-bit rows (gg_fp4_dequantize): codes uint8 [..., k / 2]
+    and their packed scales; rows no expert owns are left untouched."""
+    torch = _torch()
+    lead, rows, half, e = _fp4_rows(layout, codes, "codes", torch.uint8, groups)
+    if half % 16:
+        raise ValueError("codes must have a multiple of 16 columns (32 values)")
+    if scales is None:
+        raise ValueError("scales are required")
+    _packed4(scales, "scales", layout, rows, 2 * half, e, codes.device)
+    out = _shaped(out, "out", torch.bfloat16, (*lead, 2 * half), codes.device)
+    _launch("gg_fp4_dequantize", codes.device, int(layout), _ptr(codes), _ptr(scales), _ptr(groups), rows, 2 * half, e,
+            _ptr(out))
+    return out
+
+
+def fp4_gather_rows(src, row_slot, topk, offs, out=None, out_scales=None):
+    """Token rows sorted by expert into 4-bit rows (gg_fp4_gather_rows): src
+    bf16 [tokens, k]; row_slot and offs from ``route``.  Returns (codes
+    [len(row_slot), k / 2], packed scales) as ``fp4_forward`` takes them; rows
+    past offs[-1] are left untouched."""
+    torch = _torch()
+    dev = src.device
+    _check(src, "src", torch.bfloat16, 2, dev)
+    tokens, k = src.shape
+    if k % 32:
+        raise ValueError("src must have a multiple of 32 columns")
+    _check(row_slot, "row_slot", torch.int32, 1, dev)
+    _check(offs, "offs", torch.int32, 1, dev)
+    cap, e = row_slot.shape[0], offs.shape[0]
+    out = _shaped(out, "out", torch.uint8, (cap, k // 2), dev)
+    out_scales = _packed4(out_scales, "out_scales", GG_FP4_ACT_RAGGED, cap, k, e, dev)
+    _launch("gg_fp4_gather_rows", dev, _ptr(src), tokens, k, _ptr(row_slot), int(topk), _ptr(offs), e, cap, _ptr(out),
+            _ptr(out_scales))
+    return out, out_scales
+
+
+def fp4_silu_mul_rows(h, groups, masked=False, out=None, out_scales=None):
+    """4-bit rows of silu(gate) * up (gg_fp4_silu_mul_rows): h bf16 [m, 2I]
+    (masked: [E, max_m, 2I]; gate columns first), I a multiple of 32.  Returns
+    (codes uint8 [..., I / 2], packed scales)."""
+    torch = _torch()
+    lead, m, n = _grouped(h, "h", torch.bfloat16, groups, masked)
+    if n % 64:
+        raise ValueError("h must have 2 I columns with I a multiple of 32")
+    out = _shaped(out, "out", torch.uint8, (*lead, n // 4), h.device)
+    out_scales = _packed4(out_scales, "out_scales", GG_FP4_ACT_MASKED if masked else GG_FP4_ACT_RAGGED, m, n // 2,
+                          groups.shape[0], h.device)
+    _launch("gg_fp4_masked_silu_mul_rows" if masked else "gg_fp4_silu_mul_rows", h.device, _ptr(h), _ptr(groups),
+            _ptr(out), _ptr(out_scales), m, n, groups.shape[0])
+    return out, out_scales
+
+
+def _fp4_forward(name, layout, x, x_scales, w, w_scales, groups, out, out_dtype):
+    torch = _torch()
+    lead, m, half, e = _fp4_rows(layout, x, "x", torch.uint8, groups)
+    dev = x.device
+    _check(w, "w", torch.uint8, 3, dev)
+    n = w.shape[1]
+    if w.shape[0] != e or w.shape[2] != half:
+        raise ValueError("shape mismatch between x, w and groups")
+    if half % 16:
+        raise ValueError("x must have a multiple of 16 columns (32 values)")
+    if x_scales is None or w_scales is None:
+        raise ValueError("x_scales and w_scales are required")
+    _packed4(x_scales, "x_scales", layout, m, 2 * half, e, dev)
+    _packed4(w_scales, "w_scales", GG_FP4_WEIGHT, n, 2 * half, e, dev)
+    out = _shaped(out, "out", (out_dtype or torch.bfloat16) if out is None else out.dtype, (*lead, n), dev)
+    _launch(name, dev, _ptr(x), _ptr(x_scales), _ptr(w), _ptr(w_scales), _ptr(groups), _ptr(out),
+            _dtype_code(out.dtype), m, 2 * half, n, e)
+    return out
+
+
+def fp4_forward(x, x_scales, w, w_scales, offs, out=None, out_dtype=None):
+    """Y[rows of g] = sum_k x sx w[g] sw (gg_fp4_forward).  x: 4-bit rows
+    uint8 [m, k / 2] with packed scales (GG_FP4_ACT_RAGGED, the same offs); w:
+    uint8 [E, n, k / 2] with packed scales (GG_FP4_WEIGHT)."""
+    return _fp4_forward("gg_fp4_forward", GG_FP4_ACT_RAGGED, x, x_scales, w, w_scales, offs, out, out_dtype)
+
+
+def fp4_masked_forward(x, x_scales, w, w_scales, masked_m, out=None, out_dtype=None):
+    """The masked 4-bit forward (gg_fp4_masked_forward): x uint8 [E, max_m,
+    k / 2], x_scales packed with GG_FP4_ACT_MASKED and the same masked_m."""
+    return _fp4_forward("gg_fp4_masked_forward", GG_FP4_ACT_MASKED, x, x_scales, w, w_scales, masked_m, out, out_dtype)

@@ -780,6 +780,142 @@ gg_status gg_masked_silu_mul_grad(const void* da, const void* h, const void* h_s
   return silu_grad_run(true, da, h, h_scales, masked_m, dh, act, max_m, n, num_groups, stream);
 }
 
+// ---- 4-bit rows and weights ------------------------------------------------------------
+
+static bool fp4_dims(int64_t k) { return k >= 32 && k % 32 == 0 && k <= GG_MAX_KN; }
+
+int64_t gg_fp4_scale_bytes(gg_fp4_layout layout, int64_t rows, int64_t k, int32_t num_groups) {
+  if (layout < GG_FP4_ACT_RAGGED || layout > GG_FP4_WEIGHT || !fp4_dims(k)) return -1;
+  if (num_groups < 1 || num_groups > GG_MAX_GROUPS || rows < 0 || rows >= kRowLimit) return -1;
+  return gg::fp4_scale_tiles((int)layout, rows, num_groups) * ((k + 127) / 128) * 1024;
+}
+
+// a, b: the operands whose rows the layout describes; scales: the packed ones.
+static gg_status fp4_check(int layout, const void* a, const void* b, const void* scales, const int32_t* groups,
+                           int64_t rows, int64_t k, int32_t E) {
+  if (layout < GG_FP4_ACT_RAGGED || layout > GG_FP4_WEIGHT) return fail(GG_ERR_BAD_DIM, "unknown layout");
+  if ((layout != GG_FP4_WEIGHT && !groups) || (rows > 0 && (!a || !b || !scales)))
+    return fail(GG_ERR_NULL_PTR, "a required pointer is NULL");
+  if (E < 1 || E > GG_MAX_GROUPS) return fail(GG_ERR_LIMIT, "num_groups must be in [1, GG_MAX_GROUPS]");
+  if (rows < 0 || !fp4_dims(k))
+    return fail(GG_ERR_BAD_DIM, "need rows >= 0 and k a positive multiple of 32 up to GG_MAX_KN");
+  if (rows >= kRowLimit || (layout != GG_FP4_ACT_RAGGED && (double)rows * E >= (double)kRowLimit))
+    return fail(GG_ERR_BAD_DIM, "row count must be below 2^31 - 2^16");
+  if (!aligned16(a) || !aligned16(b) || !aligned16(scales) || !aligned4(groups))
+    return fail(GG_ERR_ALIGNMENT, "pointers must be 16-byte aligned");
+  return GG_OK;
+}
+
+gg_status gg_fp4_pack_scales(gg_fp4_layout layout, const void* src, int64_t ld_src, const int32_t* groups,
+                             int64_t rows, int64_t k, int32_t num_groups, void* dst, void* stream) {
+  gg_status s = fp4_check(layout, dst, dst, dst, groups, rows, k, num_groups);
+  if (s != GG_OK) return s;
+  if (rows > 0 && !src) return fail(GG_ERR_NULL_PTR, "a required pointer is NULL");
+  if (ld_src < k / 32) return fail(GG_ERR_BAD_DIM, "ld_src must be at least k / 32");
+  if ((double)rows * num_groups * (double)ld_src > 4.0e18) return fail(GG_ERR_BAD_DIM, "problem too large");
+  int cus = 0;
+  s = device_cus(&cus);
+  if (s != GG_OK) return s;
+  return hip_result(gg::launch_fp4_pack_scales((int)layout, src, ld_src, groups, rows, k, num_groups, dst, cus,
+                                               static_cast<hipStream_t>(stream)));
+}
+
+gg_status gg_fp4_quantize(gg_fp4_layout layout, const void* x, const int32_t* groups, int64_t rows, int64_t k,
+                          int32_t num_groups, void* codes, void* scales, void* stream) {
+  gg_status s = fp4_check(layout, x, codes, scales, groups, rows, k, num_groups);
+  if (s != GG_OK) return s;
+  int cus = 0;
+  s = device_cus(&cus);
+  if (s != GG_OK) return s;
+  return hip_result(gg::launch_fp4_quantize((int)layout, x, groups, rows, k, num_groups, codes, scales, cus,
+                                            static_cast<hipStream_t>(stream)));
+}
+
+gg_status gg_fp4_gather_rows(const void* src, int64_t tokens, int64_t k, const int32_t* row_slot, int32_t topk,
+                             const int32_t* offs, int32_t num_groups, int64_t rows_cap, void* codes, void* scales,
+                             void* stream) {
+  gg_status s = fp4_check(GG_FP4_ACT_RAGGED, codes, codes, scales, offs, rows_cap, k, num_groups);
+  if (s != GG_OK) return s;
+  if ((tokens > 0 && !src) || (rows_cap > 0 && !row_slot)) return fail(GG_ERR_NULL_PTR, "a required pointer is NULL");
+  if (tokens < 0 || topk < 1) return fail(GG_ERR_BAD_DIM, "need tokens >= 0, topk >= 1");
+  if (tokens >= kRowLimit || tokens * (int64_t)topk >= kRowLimit)
+    return fail(GG_ERR_BAD_DIM, "row and slot counts must be below 2^31 - 2^16");
+  if (!aligned16(src) || !aligned4(row_slot)) return fail(GG_ERR_ALIGNMENT, "pointers must be 16-byte aligned");
+  int cus = 0;
+  s = device_cus(&cus);
+  if (s != GG_OK) return s;
+  return hip_result(gg::launch_fp4_gather_rows(src, tokens, k, row_slot, topk, offs, num_groups, rows_cap, codes,
+                                               scales, cus, static_cast<hipStream_t>(stream)));
+}
+
+static gg_status fp4_silu_run(bool masked, const void* h, const int32_t* groups, void* codes, void* scales, int64_t m,
+                              int64_t n, int32_t E, void* stream) {
+  if (n > GG_MAX_KN || n < 64 || n % 64 != 0)
+    return fail(GG_ERR_BAD_DIM, "need n (= 2 I) a positive multiple of 64 up to GG_MAX_KN");
+  gg_status s = fp4_check(masked ? GG_FP4_ACT_MASKED : GG_FP4_ACT_RAGGED, h, codes, scales, groups, m, n / 2, E);
+  if (s != GG_OK) return s;
+  int cus = 0;
+  s = device_cus(&cus);
+  if (s != GG_OK) return s;
+  return hip_result(gg::launch_fp4_silu_mul_rows(masked, h, groups, E, m, n / 2, codes, scales, cus,
+                                                 static_cast<hipStream_t>(stream)));
+}
+
+gg_status gg_fp4_silu_mul_rows(const void* h, const int32_t* offs, void* codes, void* scales, int64_t m, int64_t n,
+                               int32_t num_groups, void* stream) {
+  return fp4_silu_run(false, h, offs, codes, scales, m, n, num_groups, stream);
+}
+
+gg_status gg_fp4_masked_silu_mul_rows(const void* h, const int32_t* masked_m, void* codes, void* scales, int64_t max_m,
+                                      int64_t n, int32_t num_groups, void* stream) {
+  return fp4_silu_run(true, h, masked_m, codes, scales, max_m, n, num_groups, stream);
+}
+
+gg_status gg_fp4_dequantize(gg_fp4_layout layout, const void* codes, const void* scales, const int32_t* groups,
+                            int64_t rows, int64_t k, int32_t num_groups, void* out, void* stream) {
+  gg_status s = fp4_check(layout, codes, out, scales, groups, rows, k, num_groups);
+  if (s != GG_OK) return s;
+  int cus = 0;
+  s = device_cus(&cus);
+  if (s != GG_OK) return s;
+  return hip_result(gg::launch_fp4_dequantize((int)layout, codes, scales, groups, rows, k, num_groups, out, cus,
+                                              static_cast<hipStream_t>(stream)));
+}
+
+static gg_status fp4_run(bool masked, const void* x, const void* xs, const void* w, const void* ws,
+                         const int32_t* groups, void* y, gg_dtype y_dtype, int64_t rows, int64_t k, int64_t n,
+                         int32_t E, void* stream) {
+  if (rows == 0) x = xs = y = const_cast<void*>(w);      // nothing is read or written: these may be NULL
+  if (!groups) return fail(GG_ERR_NULL_PTR, "a required pointer is NULL");
+  if (!aligned4(groups)) return fail(GG_ERR_ALIGNMENT, "int32 arrays must be 4-byte aligned");
+  gg_status s = check(x, w, w, y, y_dtype, rows, k, n, E);
+  if (s != GG_OK) return s;
+  if (!xs || !ws) return fail(GG_ERR_NULL_PTR, "a required pointer is NULL");
+  if (k % 32 != 0) return fail(GG_ERR_BAD_DIM, "k must be a multiple of 32 (one scale per 32 values)");
+  if (!aligned16(xs) || !aligned16(ws)) return fail(GG_ERR_ALIGNMENT, "pointers must be 16-byte aligned");
+  if (masked) {
+    s = masked_rows(rows, E);
+    if (s != GG_OK) return s;
+  }
+  if (rows == 0) return GG_OK;
+  int cus = 0;
+  s = device_cus(&cus);
+  if (s != GG_OK) return s;
+  return hip_result(gg::launch_fp4(masked, x, xs, w, ws, groups, y, y_dtype == GG_F32, rows, k, n, E, cus,
+                                   static_cast<hipStream_t>(stream)));
+}
+
+gg_status gg_fp4_forward(const void* x, const void* x_scales, const void* w, const void* w_scales, const int32_t* offs,
+                         void* y, gg_dtype y_dtype, int64_t m, int64_t k, int64_t n, int32_t num_groups, void* stream) {
+  return fp4_run(false, x, x_scales, w, w_scales, offs, y, y_dtype, m, k, n, num_groups, stream);
+}
+
+gg_status gg_fp4_masked_forward(const void* x, const void* x_scales, const void* w, const void* w_scales,
+                                const int32_t* masked_m, void* y, gg_dtype y_dtype, int64_t max_m, int64_t k,
+                                int64_t n, int32_t num_groups, void* stream) {
+  return fp4_run(true, x, x_scales, w, w_scales, masked_m, y, y_dtype, max_m, k, n, num_groups, stream);
+}
+
 const char* gg_status_str(gg_status s) {
   switch (s) {
     case GG_OK: return "GG_OK";

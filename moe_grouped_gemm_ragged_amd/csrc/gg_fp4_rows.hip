@@ -1,0 +1,382 @@
+// gg_fp4_rows.hip -- bf16 rows to 4 bits and back (see gg_fp4.h for the rows
+// and the packed layout of their scales).
+//
+//   plain    codes of x's rows
+//   gather   codes of token rows sorted by expert, zero codes and the scale 1
+//            for a padding row
+//   silu     codes of a = silu(g) u of gate/up rows h = [g | u]
+//   back     code * scale, in bf16
+//   pack     scale bytes [rows, k / 32], as a checkpoint holds them, to the
+//            packed layout
+//
+// All of them walk units of half a tile (128 rows) by two stages (256
+// values): the unit's scales are then 1024 bytes of the packed layout that
+// one workgroup assembles in LDS and writes whole, where rows one at a time
+// would write single bytes 1 KB apart.  A row's part of a unit is 512 bytes
+// of bf16 and 128 of codes, 32 lanes with 8 values each; 4 lanes hold a
+// block, so its largest value is two lane exchanges away.  Bound by memory.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "gg_fp4.h"
+#include "gg_internal.h"
+#include "gg_rows.h"
+
+namespace gg {
+namespace {
+
+using namespace rows;
+using namespace fp4;
+
+constexpr int kThreads = 256;
+constexpr int kHalf = 128;           // rows of a unit
+constexpr int kRowsAtOnce = 8;       // of them at a time: 32 lanes each
+constexpr int kUnitStages = 2;
+
+enum Source { PLAIN = 0, GATHER = 1, SILU = 2 };
+
+// Block-wide inclusive scan of one non-negative int per thread; *excl gets
+// the exclusive value (0 for thread 0).
+template <bool MAX>
+__device__ __forceinline__ int block_scan(int v, int* wave_tot, int tid, int* excl) {
+  const int lane = tid & 63, w = tid >> 6;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int o = __shfl_up(v, (unsigned)d, 64);
+    if (lane >= d) v = MAX ? (v > o ? v : o) : v + o;
+  }
+  int prev = __shfl_up(v, 1u, 64);
+  if (lane == 0) prev = 0;
+  if (lane == 63) wave_tot[w] = v;
+  __syncthreads();
+  int before = 0;
+  for (int q = 0; q < w; ++q) {
+    const int t = wave_tot[q];
+    before = MAX ? (before > t ? before : t) : before + t;
+  }
+  __syncthreads();
+  *excl = MAX ? (prev > before ? prev : before) : prev + before;
+  return MAX ? (v > before ? v : before) : v + before;
+}
+
+// The tiles of a layout: ragged experts' clamped ends and the tiles before
+// each, decoded from the offsets as the product decodes them.
+struct Tiles {
+  int32_t end[GG_MAX_GROUPS_DEV];
+  int32_t pref[GG_MAX_GROUPS_DEV + 1];
+  int32_t wave[kThreads / 64];
+};
+struct NoTiles {};
+
+// Returns the number of tiles.
+__device__ __forceinline__ int64_t decode_tiles(Tiles& s, const int32_t* groups, int64_t rows, int E, int tid) {
+  const int per = (E + kThreads - 1) / kThreads;
+  const int g0 = tid * per;
+  const int g1 = g0 + per < E ? g0 + per : E;
+  int run = 0;
+  for (int g = g0; g < g1; ++g) {
+    const int o = groups[g];
+    run = o > run ? o : run;
+    s.end[g] = run;
+  }
+  int before;
+  block_scan<true>(run, s.wave, tid, &before);
+  for (int g = g0; g < g1; ++g) {
+    const int e = s.end[g] > before ? s.end[g] : before;
+    s.end[g] = e < rows ? e : (int)rows;
+  }
+  __syncthreads();
+  int local = 0;
+  for (int g = g0; g < g1; ++g) local += (s.end[g] - (g == 0 ? 0 : s.end[g - 1]) + kTileRows - 1) / kTileRows;
+  int acc;
+  const int incl = block_scan<false>(local, s.wave, tid, &acc);
+  for (int g = g0; g < g1; ++g) {
+    s.pref[g] = acc;
+    acc += (s.end[g] - (g == 0 ? 0 : s.end[g - 1]) + kTileRows - 1) / kTileRows;
+  }
+  if (tid == kThreads - 1) s.pref[E] = incl;
+  __syncthreads();
+  return s.pref[E];
+}
+
+// The first row of tile T and how many of its 256 rows are an expert's.
+template <int LAYOUT, typename S>
+__device__ __forceinline__ void tile_rows(const S& s, const int32_t* groups, int64_t rows, int E, int64_t T,
+                                          int64_t& first, int& valid) {
+  if constexpr (LAYOUT == RAGGED) {
+    int lo = 0, hi = E;                 // largest g with pref[g] <= T
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (s.pref[mid] <= T) lo = mid; else hi = mid;
+    }
+    first = (lo == 0 ? 0 : s.end[lo - 1]) + (T - s.pref[lo]) * kTileRows;
+    const int64_t v = s.end[lo] - first;
+    valid = v < kTileRows ? (int)v : kTileRows;
+  } else {
+    const int64_t per = (rows + kTileRows - 1) / kTileRows;
+    const int64_t e = T / per, r0 = (T - e * per) * kTileRows;
+    int64_t active = rows;
+    if constexpr (LAYOUT == MASKED_ROWS) {
+      const int64_t a = groups[e];
+      active = a < 0 ? 0 : a < rows ? a : rows;
+    }
+    first = e * rows + r0;
+    const int64_t v = active - r0;
+    valid = v < 0 ? 0 : v < kTileRows ? (int)v : kTileRows;
+  }
+}
+
+struct In {
+  const uint16_t* x;         // plain: rows; gather: token rows; silu: gate/up rows of 2 k values
+  const int32_t* row_slot;   // gather
+  int32_t topk;
+  int64_t tokens;
+};
+
+__device__ __forceinline__ float sigmoid(float g) { return __builtin_amdgcn_rcpf(1.0f + __expf(-g)); }
+
+template <int LAYOUT, int SRC>
+__global__ __launch_bounds__(kThreads) void to4_kernel(In in, const int32_t* groups, int64_t rows, int64_t k, int32_t E,
+                                                       int64_t tiles, uint8_t* codes, uint8_t* scales) {
+  __shared__ std::conditional_t<LAYOUT == RAGGED, Tiles, NoTiles> s_tiles;
+  __shared__ uint32_t s_sc[kUnitStages * kStageBytes / 2 / 4];     // [stage][half tile]
+  const int tid = threadIdx.x;
+  if constexpr (LAYOUT == RAGGED) tiles = decode_tiles(s_tiles, groups, rows, E, tid);
+  const int64_t stages = stages4(k);
+  const int64_t across = (stages + kUnitStages - 1) / kUnitStages;
+  const int lane = tid & 31, rsub = tid >> 5;
+  uint8_t* const my = reinterpret_cast<uint8_t*>(s_sc) + 512 * (lane >> 4);
+  const int q = (lane & 15) >> 2;
+  for (int64_t u = blockIdx.x; u < 2 * tiles * across; u += gridDim.x) {
+    const int64_t th = u / across;
+    const int64_t s0 = (u - th * across) * kUnitStages;
+    const int half = (int)(th & 1);
+    int64_t first;
+    int valid;
+    tile_rows<LAYOUT>(s_tiles, groups, rows, E, th >> 1, first, valid);
+    if (valid <= 0) continue;                    // (masked: a tile without rows)
+    valid -= kHalf * half;
+    first += kHalf * half;
+    const int64_t col = s0 * kStage4 + 8 * lane;
+    s_sc[tid] = 0u;
+    __syncthreads();
+    if (col < k) {
+      constexpr int kAhead = 4;
+      for (int r0 = rsub; r0 < valid && r0 < kHalf; r0 += kRowsAtOnce * kAhead) {
+        u32x4r g[kAhead], up[SRC == SILU ? kAhead : 1];
+        bool pad[kAhead];
+#pragma unroll
+        for (int a = 0; a < kAhead; ++a) {
+          const int r = r0 + kRowsAtOnce * a;
+          pad[a] = false;
+          g[a] = u32x4r{0u, 0u, 0u, 0u};
+          if (r < valid && r < kHalf) {
+            if constexpr (SRC == PLAIN) {
+              g[a] = load16(in.x + (first + r) * k + col);
+            } else if constexpr (SRC == SILU) {
+              g[a] = load16(in.x + (first + r) * 2 * k + col);
+              up[a] = load16(in.x + (first + r) * 2 * k + k + col);
+            } else {
+              const int32_t slot = in.row_slot[first + r];
+              const int32_t t = slot / in.topk;
+              pad[a] = slot < 0 || t >= in.tokens;
+              if (!pad[a]) g[a] = load16(in.x + (int64_t)t * k + col);
+            }
+          }
+        }
+#pragma unroll
+        for (int a = 0; a < kAhead; ++a) {
+          const int r = r0 + kRowsAtOnce * a;
+          if (r < valid && r < kHalf) {
+            float v[8];
+            unpack8(g[a], v);
+            if constexpr (SRC == SILU) {
+              float w[8];
+              unpack8(up[a], w);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) v[e] = v[e] * sigmoid(v[e]) * w[e];
+            }
+            int byte;
+            const uint32_t c = quantise4(v, byte);
+            *reinterpret_cast<uint32_t*>(codes + (first + r) * (k / 2) + col / 2) = c;
+            if ((lane & 3) == 0) my[scale_place(r, q)] = (uint8_t)byte;
+          }
+        }
+      }
+    }
+    __syncthreads();
+    const int64_t st = s0 + (tid >> 7);
+    if (st < stages)
+      reinterpret_cast<uint32_t*>(scales + ((th >> 1) * stages + st) * kStageBytes + 512 * half)[tid & 127] = s_sc[tid];
+    __syncthreads();
+  }
+}
+
+template <int LAYOUT>
+__global__ __launch_bounds__(kThreads) void from4_kernel(const uint8_t* codes, const uint8_t* scales,
+                                                         const int32_t* groups, int64_t rows, int64_t k, int32_t E,
+                                                         int64_t tiles, uint16_t* out) {
+  __shared__ std::conditional_t<LAYOUT == RAGGED, Tiles, NoTiles> s_tiles;
+  __shared__ uint32_t s_sc[kUnitStages * kStageBytes / 2 / 4];
+  const int tid = threadIdx.x;
+  if constexpr (LAYOUT == RAGGED) tiles = decode_tiles(s_tiles, groups, rows, E, tid);
+  const int64_t stages = stages4(k);
+  const int64_t across = (stages + kUnitStages - 1) / kUnitStages;
+  const int lane = tid & 31, rsub = tid >> 5;
+  const uint8_t* const my = reinterpret_cast<const uint8_t*>(s_sc) + 512 * (lane >> 4);
+  const int q = (lane & 15) >> 2;
+  for (int64_t u = blockIdx.x; u < 2 * tiles * across; u += gridDim.x) {
+    const int64_t th = u / across;
+    const int64_t s0 = (u - th * across) * kUnitStages;
+    const int half = (int)(th & 1);
+    int64_t first;
+    int valid;
+    tile_rows<LAYOUT>(s_tiles, groups, rows, E, th >> 1, first, valid);
+    valid -= kHalf * half;
+    first += kHalf * half;
+    if (valid <= 0) continue;
+    const int64_t col = s0 * kStage4 + 8 * lane;
+    const int64_t st = s0 + (tid >> 7);
+    if (st < stages)
+      s_sc[tid] =
+          reinterpret_cast<const uint32_t*>(scales + ((th >> 1) * stages + st) * kStageBytes + 512 * half)[tid & 127];
+    __syncthreads();
+    if (col < k) {
+      constexpr int kAhead = 4;
+      for (int r0 = rsub; r0 < valid && r0 < kHalf; r0 += kRowsAtOnce * kAhead) {
+        uint32_t c[kAhead];
+#pragma unroll
+        for (int a = 0; a < kAhead; ++a) {
+          const int r = r0 + kRowsAtOnce * a;
+          c[a] = 0u;
+          if (r < valid && r < kHalf) c[a] = *reinterpret_cast<const uint32_t*>(codes + (first + r) * (k / 2) + col / 2);
+        }
+#pragma unroll
+        for (int a = 0; a < kAhead; ++a) {
+          const int r = r0 + kRowsAtOnce * a;
+          if (r < valid && r < kHalf) {
+            // the conversion takes the scale's exponent bits alone, as an E8M0 byte
+            const float s = __builtin_bit_cast(float, (uint32_t)my[scale_place(r, q)] << 23);
+            u32x4r o;
+            o[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c[a], s, 0));
+            o[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c[a], s, 1));
+            o[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c[a], s, 2));
+            o[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c[a], s, 3));
+            store16(out + (first + r) * k + col, o);
+          }
+        }
+      }
+    }
+    __syncthreads();
+  }
+}
+
+// Thread t writes dword t of a unit: the 4 rows of its place, one block.
+template <int LAYOUT>
+__global__ __launch_bounds__(kThreads) void pack4_kernel(const uint8_t* src, int64_t ld_src, const int32_t* groups,
+                                                         int64_t rows, int64_t k, int32_t E, int64_t tiles,
+                                                         uint8_t* scales) {
+  __shared__ std::conditional_t<LAYOUT == RAGGED, Tiles, NoTiles> s_tiles;
+  const int tid = threadIdx.x;
+  if constexpr (LAYOUT == RAGGED) tiles = decode_tiles(s_tiles, groups, rows, E, tid);
+  const int64_t stages = stages4(k), blocks = k / kBlock4;
+  const int64_t across = (stages + kUnitStages - 1) / kUnitStages;
+  const int d = tid & 127;
+  for (int64_t u = blockIdx.x; u < 2 * tiles * across; u += gridDim.x) {
+    const int64_t th = u / across;
+    const int64_t st = (u - th * across) * kUnitStages + (tid >> 7);
+    const int half = (int)(th & 1);
+    int64_t first;
+    int valid;
+    tile_rows<LAYOUT>(s_tiles, groups, rows, E, th >> 1, first, valid);
+    if (valid <= 0 || st >= stages) continue;
+    const int64_t b = 4 * st + 2 * (d & 1) + ((d >> 1) & 1);
+    uint32_t word = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = kHalf * half + (d >> 2) + 32 * i;
+      if (r < valid && b < blocks) word |= (uint32_t)src[(first + r) * ld_src + b] << (8 * i);
+    }
+    reinterpret_cast<uint32_t*>(scales + ((th >> 1) * stages + st) * kStageBytes + 512 * half)[d] = word;
+  }
+}
+
+int grid_for(int64_t tiles, int64_t k, int num_cus) {
+  const int64_t units = 2 * tiles * ((stages4(k) + kUnitStages - 1) / kUnitStages);
+  const int64_t most = 8 * (int64_t)num_cus;
+  return (int)(units < most ? units : most);
+}
+
+template <int LAYOUT>
+hipError_t to4(const In& in, const int32_t* groups, int64_t rows, int64_t k, int32_t E, void* codes, void* scales,
+               int num_cus, hipStream_t stream) {
+  const int64_t tiles = fp4_scale_tiles(LAYOUT, rows, E);
+  auto* kernel = to4_kernel<LAYOUT, PLAIN>;
+  return launch_kernel(kernel, dim3(grid_for(tiles, k, num_cus)), dim3(kThreads), stream, in, groups, rows, k, E,
+                       tiles, static_cast<uint8_t*>(codes), static_cast<uint8_t*>(scales));
+}
+
+}  // namespace
+
+int64_t fp4_scale_tiles(int layout, int64_t rows, int32_t num_groups) {
+  const int64_t t = (rows + kTileRows - 1) / kTileRows;
+  return layout == RAGGED ? t + num_groups : t * num_groups;
+}
+
+hipError_t launch_fp4_quantize(int layout, const void* x, const int32_t* groups, int64_t rows, int64_t k, int32_t E,
+                               void* codes, void* scales, int num_cus, hipStream_t stream) {
+  if (rows == 0) return hipSuccess;
+  const In in = {static_cast<const uint16_t*>(x), nullptr, 1, 0};
+  switch (layout) {
+    case RAGGED: return to4<RAGGED>(in, groups, rows, k, E, codes, scales, num_cus, stream);
+    case MASKED_ROWS: return to4<MASKED_ROWS>(in, groups, rows, k, E, codes, scales, num_cus, stream);
+    default: return to4<WEIGHTS>(in, groups, rows, k, E, codes, scales, num_cus, stream);
+  }
+}
+
+hipError_t launch_fp4_gather_rows(const void* src, int64_t tokens, int64_t k, const int32_t* row_slot, int32_t topk,
+                                  const int32_t* offs, int32_t E, int64_t rows_cap, void* codes, void* scales,
+                                  int num_cus, hipStream_t stream) {
+  if (rows_cap == 0) return hipSuccess;
+  const In in = {static_cast<const uint16_t*>(src), row_slot, topk, tokens};
+  const int64_t tiles = fp4_scale_tiles(RAGGED, rows_cap, E);
+  return launch_kernel(to4_kernel<RAGGED, GATHER>, dim3(grid_for(tiles, k, num_cus)), dim3(kThreads), stream, in, offs,
+                       rows_cap, k, E, tiles, static_cast<uint8_t*>(codes), static_cast<uint8_t*>(scales));
+}
+
+hipError_t launch_fp4_silu_mul_rows(bool masked, const void* h, const int32_t* groups, int32_t E, int64_t m,
+                                    int64_t width, void* codes, void* scales, int num_cus, hipStream_t stream) {
+  if (m == 0) return hipSuccess;
+  const In in = {static_cast<const uint16_t*>(h), nullptr, 1, 0};
+  const int layout = masked ? MASKED_ROWS : RAGGED;
+  const int64_t tiles = fp4_scale_tiles(layout, m, E);
+  auto* kernel = masked ? to4_kernel<MASKED_ROWS, SILU> : to4_kernel<RAGGED, SILU>;
+  return launch_kernel(kernel, dim3(grid_for(tiles, width, num_cus)), dim3(kThreads), stream, in, groups, m, width, E,
+                       tiles, static_cast<uint8_t*>(codes), static_cast<uint8_t*>(scales));
+}
+
+hipError_t launch_fp4_dequantize(int layout, const void* codes, const void* scales, const int32_t* groups, int64_t rows,
+                                 int64_t k, int32_t E, void* out, int num_cus, hipStream_t stream) {
+  if (rows == 0) return hipSuccess;
+  const int64_t tiles = fp4_scale_tiles(layout, rows, E);
+  auto* kernel = layout == RAGGED        ? from4_kernel<RAGGED>
+                 : layout == MASKED_ROWS ? from4_kernel<MASKED_ROWS>
+                                         : from4_kernel<WEIGHTS>;
+  return launch_kernel(kernel, dim3(grid_for(tiles, k, num_cus)), dim3(kThreads), stream,
+                       static_cast<const uint8_t*>(codes), static_cast<const uint8_t*>(scales), groups, rows, k, E,
+                       tiles, static_cast<uint16_t*>(out));
+}
+
+hipError_t launch_fp4_pack_scales(int layout, const void* src, int64_t ld_src, const int32_t* groups, int64_t rows,
+                                  int64_t k, int32_t E, void* dst, int num_cus, hipStream_t stream) {
+  if (rows == 0) return hipSuccess;
+  const int64_t tiles = fp4_scale_tiles(layout, rows, E);
+  auto* kernel = layout == RAGGED        ? pack4_kernel<RAGGED>
+                 : layout == MASKED_ROWS ? pack4_kernel<MASKED_ROWS>
+                                         : pack4_kernel<WEIGHTS>;
+  return launch_kernel(kernel, dim3(grid_for(tiles, k, num_cus)), dim3(kThreads), stream,
+                       static_cast<const uint8_t*>(src), ld_src, groups, rows, k, E, tiles,
+                       static_cast<uint8_t*>(dst));
+}
+
+}  // namespace gg

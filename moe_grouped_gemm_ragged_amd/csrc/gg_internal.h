@@ -53,6 +53,28 @@ hipError_t launch_fp8(bool masked, const void* x, const void* sx, const void* w,
                       const int32_t* groups, void* c, bool out_f32, int64_t m, int64_t k, int64_t n,
                       int32_t num_groups, int num_cus, hipStream_t stream);
 
+// The same on 4-bit operands: two e2m1 codes a byte, x [rows, k / 2] and w
+// [E, n, k / 2], scales in the packed layout of gg_fp4.h, k a multiple of 32.
+hipError_t launch_fp4(bool masked, const void* x, const void* sx, const void* w, const void* sw,
+                      const int32_t* groups, void* c, bool out_f32, int64_t m, int64_t k, int64_t n,
+                      int32_t num_groups, int num_cus, hipStream_t stream);
+
+// bf16 rows to 4 bits and back (gg_fp4_rows.hip).  layout: 0 ragged rows
+// (groups = end offsets), 1 masked (groups = masked_m, rows = max_m), 2
+// weights (rows of each expert, groups unused).
+int64_t fp4_scale_tiles(int layout, int64_t rows, int32_t num_groups);
+hipError_t launch_fp4_quantize(int layout, const void* x, const int32_t* groups, int64_t rows, int64_t k, int32_t E,
+                               void* codes, void* scales, int num_cus, hipStream_t stream);
+hipError_t launch_fp4_gather_rows(const void* src, int64_t tokens, int64_t k, const int32_t* row_slot, int32_t topk,
+                                  const int32_t* offs, int32_t E, int64_t rows_cap, void* codes, void* scales,
+                                  int num_cus, hipStream_t stream);
+hipError_t launch_fp4_silu_mul_rows(bool masked, const void* h, const int32_t* groups, int32_t E, int64_t m,
+                                    int64_t width, void* codes, void* scales, int num_cus, hipStream_t stream);
+hipError_t launch_fp4_dequantize(int layout, const void* codes, const void* scales, const int32_t* groups, int64_t rows,
+                                 int64_t k, int32_t E, void* out, int num_cus, hipStream_t stream);
+hipError_t launch_fp4_pack_scales(int layout, const void* src, int64_t ld_src, const int32_t* groups, int64_t rows,
+                                  int64_t k, int32_t E, void* dst, int num_cus, hipStream_t stream);
+
 // The weight gradient from e4m3 activations: x [rows, k] e4m3 with scales sx
 // in the packed layout, dy bf16, dw[g] = alpha * x^T dy + beta * dw[g].
 // Arguments were validated by the caller.

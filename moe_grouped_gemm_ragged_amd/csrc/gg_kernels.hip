@@ -99,7 +99,8 @@ typedef short shortx4 __attribute__((ext_vector_type(4)));
 
 enum Mode {
   FWD = 0, DGRAD = 1, WGRAD = 2, MASKED = 3, MASKED_DGRAD = 4, MASKED_WGRAD = 5,
-  FWD_SILU = 6, MASKED_SILU = 7, FP8 = 8, FP8_MASKED = 9, FP8_WGRAD = 10, FP8_MASKED_WGRAD = 11
+  FWD_SILU = 6, MASKED_SILU = 7, FP8 = 8, FP8_MASKED = 9, FP8_WGRAD = 10, FP8_MASKED_WGRAD = 11,
+  FP4 = 12, FP4_MASKED = 13
 };
 
 // The masked modes are the ragged passes on the masked layout: expert e's
@@ -107,11 +108,15 @@ enum Mode {
 // modes are forwards whose epilogue applies the gate/up activation.
 constexpr bool is_masked(int mode) {
   return mode == MASKED || mode == MASKED_DGRAD || mode == MASKED_WGRAD || mode == MASKED_SILU ||
-         mode == FP8_MASKED || mode == FP8_MASKED_WGRAD;
+         mode == FP8_MASKED || mode == FP8_MASKED_WGRAD || mode == FP4_MASKED;
 }
 // The fp8 forward modes: e4m3 operands, X [rows, K] and W [E, N, K] (both
 // reduction-contiguous), one power-of-two scale per 128 reduction values.
 constexpr bool is_fp8(int mode) { return mode == FP8 || mode == FP8_MASKED; }
+// The fp4 modes: the same with two e2m1 codes in a byte and one scale per 32
+// values (packed as gg_fp4.h states).
+constexpr bool is_fp4(int mode) { return mode == FP4 || mode == FP4_MASKED; }
+constexpr bool is_scaled(int mode) { return is_fp8(mode) || is_fp4(mode); }
 // The fp8 wgrad modes: X [rows, K] e4m3 with one power-of-two scale per row
 // and 128 columns, dY bf16.
 constexpr bool is_x8(int mode) { return mode == FP8_WGRAD || mode == FP8_MASKED_WGRAD; }
@@ -1081,6 +1086,7 @@ __device__ __attribute__((always_inline)) inline void mainloop_pp_pair(
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 constexpr int BK8 = 64;             // e4m3 values per stage
 constexpr int kScaleSlot = 512;     // LDS bytes of one k-block's scales (X, then W)
+constexpr int kScaleSlot4 = 4096;   // fp4: of a stage pair's (X of both stages, then W)
 
 // Fragment i of a stage: 32 bytes of row 32 i + l % 32 -- the two 16-byte
 // chunks the bf16 sub-steps read (chunks l / 32 and 2 + l / 32).  Which
@@ -1133,6 +1139,46 @@ __device__ __forceinline__ void scale_read(const uint8_t* slot, int wm, int wn, 
   sb >>= 16 * (wn & 1);
 }
 
+// fp4: wave w of 0..3 copies the 1024 packed bytes of X (w < 2) or W for stage
+// w mod 2 of pair `pair` into the pair's LDS slot.
+__device__ __forceinline__ void scale_load4(const uint8_t* __restrict__ sa_tile, const uint8_t* __restrict__ sb_tile,
+                                            uint32_t nbytes, int pair, uint8_t* slot, int wave, int lane) {
+  const __amdgpu_buffer_rsrc_t rs = make_rsrc(wave < 2 ? sa_tile : sb_tile, nbytes);
+  const uint32_t to = opaque_s((uint32_t)uniform(wave * 1024));
+  const uint32_t soff = (uint32_t)uniform((2 * pair + (wave & 1)) * 1024);
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, LDS_PTR(slot + to), 16, opaque_v((uint32_t)lane * 16u), soff, 0, 0);
+}
+
+// This lane's scales of stage `par` of a pair: dword ks for the fragments'
+// chunk 2 ks + l / 32, shifted so that byte i (X) / byte j (W) belongs to the
+// wave's block i / j.
+template <int TMA>
+__device__ __forceinline__ void scale_read4(const uint8_t* slot, int par, int wm, int wn, int lane, u32x2& sa,
+                                            u32x2& sb) {
+  const int wa = TMA == 2 ? 0 : wm;
+  const uint32_t at = (uint32_t)(1024 * par + 16 * (lane & 31) + 8 * (lane >> 5));
+  sa = *reinterpret_cast<const u32x2*>(slot + 512 * wa + at);
+  sb = *reinterpret_cast<const u32x2*>(slot + 2048 + 512 * (wn >> 1) + at);
+  if (TMA == 2) sa >>= (uint32_t)(16 * wm);
+  sb >>= (uint32_t)(16 * (wn & 1));
+}
+
+// One scaled MFMA of block (i, j) on half a stage's e2m1 chunks (mfma8's
+// operands and byte selects; formats 4).
+__device__ __forceinline__ floatx16 mfma4(int i, int j, const u32x4& wf, const u32x4& xf, floatx16 c, uint32_t sa,
+                                          uint32_t sb) {
+  const i32x8 w = {(int)wf[0], (int)wf[1], (int)wf[2], (int)wf[3], 0, 0, 0, 0};
+  const i32x8 x = {(int)xf[0], (int)xf[1], (int)xf[2], (int)xf[3], 0, 0, 0, 0};
+#define GG_MF4(I, J) \
+  case (I) * 2 + (J): return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w, x, c, 4, 4, J, (int)sb, I, (int)sa);
+  switch (i * 2 + j) {
+    GG_MF4(0, 0) GG_MF4(0, 1) GG_MF4(1, 0) GG_MF4(1, 1)
+    GG_MF4(2, 0) GG_MF4(2, 1) GG_MF4(3, 0) GG_MF4(3, 1)
+  }
+#undef GG_MF4
+  return c;
+}
+
 // Fragment i of a stage of X in the pair layout (the two chunks read_frag8
 // reads, at the pair layout's offsets).
 __device__ __forceinline__ i32x8 read_frag8_pair(const uint8_t* region, const FragAddr& fa, int i, int par) {
@@ -1140,6 +1186,13 @@ __device__ __forceinline__ i32x8 read_frag8_pair(const uint8_t* region, const Fr
   const u32x4 lo = *reinterpret_cast<const u32x4*>(region + fa.o[0] + d);
   const u32x4 hi = *reinterpret_cast<const u32x4*>(region + fa.o[1] + d);
   return __builtin_bit_cast(i32x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+}
+
+// 256-byte units of a packed scale tile: one per 128 values (fp8), or four
+// (fp4, whose last stage may be partly filled).
+template <int MODE>
+__device__ __forceinline__ int64_t scale_kblocks(int64_t k) {
+  return is_fp4(MODE) ? (k + 127) / 128 * 4 : k / 128;
 }
 
 // ---- fp8 ping-pong main loop ---------------------------------------------------------
@@ -1159,6 +1212,7 @@ __device__ __forceinline__ i32x8 read_frag8_pair(const uint8_t* region, const Fr
 // only) the scales of k-blocks 0 and 1, B of stage 0, its half of A pair 0,
 // B of stage 2, its half of A pair 1; group 1 its half of A pair 0, B of
 // stage 1.
+template <bool FP4>
 __device__ __attribute__((always_inline)) inline void prologue_loads8_pp(
     uint8_t* __restrict__ a0, uint8_t* __restrict__ a1, uint8_t* __restrict__ a2,
     uint8_t* __restrict__ b0, uint8_t* __restrict__ b1, uint8_t* __restrict__ b2, uint8_t* __restrict__ sc,
@@ -1170,8 +1224,13 @@ __device__ __attribute__((always_inline)) inline void prologue_loads8_pp(
   const int lane = tid & 63;
   const int w = wave & 3;
   if (wave < 4) {
-    scale_load(sa_tile, sb_tile, sc_bytes, 0, sc, wave, lane);
-    scale_load(sa_tile, sb_tile, sc_bytes, 1, sc + kScaleSlot, wave, lane);
+    if constexpr (FP4) {
+      scale_load4(sa_tile, sb_tile, sc_bytes, 0, sc, wave, lane);
+      scale_load4(sa_tile, sb_tile, sc_bytes, 1, sc + kScaleSlot4, wave, lane);
+    } else {
+      scale_load(sa_tile, sb_tile, sc_bytes, 0, sc, wave, lane);
+      scale_load(sa_tile, sb_tile, sc_bytes, 1, sc + kScaleSlot, wave, lane);
+    }
     {
       const DmaCtx c = dma_ctx_grp<false, false, 1>(B, 0, lane, w);
 #pragma unroll
@@ -1206,7 +1265,7 @@ __device__ __attribute__((always_inline)) inline void prologue_loads8_pp(
   }
 }
 
-template <int TMA>
+template <int TMA, bool FP4>
 __device__ __attribute__((always_inline)) inline void mainloop8_pp(
     uint8_t* __restrict__ a0, uint8_t* __restrict__ a1, uint8_t* __restrict__ a2, uint8_t* __restrict__ a3,
     uint8_t* __restrict__ b0, uint8_t* __restrict__ b1, uint8_t* __restrict__ b2, uint8_t* __restrict__ b3,
@@ -1216,7 +1275,9 @@ __device__ __attribute__((always_inline)) inline void mainloop8_pp(
     floatx16 (&acc)[TM][TN]) {
   A.origin = a_origin;
   B.origin = b_origin;
-  const int nk = (A.red + BK8 - 1) / BK8;           // even: K is a multiple of 128
+  // even: K is a multiple of 128 (fp8), or a last pair's second stage is
+  // zeros (fp4: A.red counts bytes, two values each)
+  const int nk = FP4 ? (A.red + 2 * BK8 - 1) / (2 * BK8) * 2 : (A.red + BK8 - 1) / BK8;
   if (nk <= 0) return;
   const int lane = tid & 63;
   const int w = wave & 3;
@@ -1227,27 +1288,45 @@ __device__ __attribute__((always_inline)) inline void mainloop8_pp(
   pp_regions_escape(rs);
   i32x8 fa[TMA], fb[TN];
   uint32_t sa = 0, sb = 0;
+  u32x2 sa4 = {0u, 0u}, sb4 = {0u, 0u};
   // group 0: the scales, B of stage 0 and its half of A pair 0 landed (the
   // last 8 loads may be in flight); group 1 waits at the next barrier
   if (g0) pp_sync<8>(rg); else pp_sync<kNoVm>(rg);
 
 #define GG8_RA(U) ((U) < 2 ? (ha ? a1 : a0) : (ha ? a3 : a2))
 #define GG8_RB(U) ((U) == 0 ? b0 : (U) == 1 ? b1 : (U) == 2 ? b2 : b3)
-// read stage U's fragments (and, for the first stage of a k-block, its
-// scales from slot (U / 2) mod 2 of the ring)
+// read stage U's fragments (and its scales from slot (U / 2) mod 2 of the
+// ring: fp8 for the first stage of a k-block, fp4 for each)
 #define GG8_PP_READ(U)                                                                            \
   {                                                                                               \
-    if (((U) & 1) == 0) scale_read<TMA>(sc + (((U) >> 1) & 1) * kScaleSlot, wm, wn, lane, sa, sb); \
+    if constexpr (FP4) scale_read4<TMA>(sc + (((U) >> 1) & 1) * kScaleSlot4, (U) & 1, wm, wn, lane, sa4, sb4); \
+    else if (((U) & 1) == 0) scale_read<TMA>(sc + (((U) >> 1) & 1) * kScaleSlot, wm, wn, lane, sa, sb); \
     _Pragma("unroll") for (int i = 0; i < TMA; ++i) fa[i] = read_frag8_pair(GG8_RA(U), faa, i, (U) & 1); \
     _Pragma("unroll") for (int j = 0; j < TN; ++j) fb[j] = read_frag8(GG8_RB(U), fab, j);        \
   }
+#define GG8_HALF(F, KS) u32x4{(uint32_t)(F)[4 * (KS)], (uint32_t)(F)[4 * (KS) + 1],                 \
+                              (uint32_t)(F)[4 * (KS) + 2], (uint32_t)(F)[4 * (KS) + 3]}
 #define GG8_PP_MFMA()                                                                             \
   {                                                                                               \
-    _Pragma("unroll") for (int q = 0; q < TMA * TN; ++q) {                                        \
-      const int i = q / TN, j = q % TN;                                                           \
-      acc[i][j] = mfma8(i, j, fb[j], fa[i], acc[i][j], sa, sb);                                   \
+    if constexpr (FP4) {                                                                          \
+      _Pragma("unroll") for (int q = 0; q < 2 * TMA * TN; ++q) {                                  \
+        const int ks = q / (TMA * TN), i = q / TN % TMA, j = q % TN;                              \
+        acc[i][j] = mfma4(i, j, GG8_HALF(fb[j], ks), GG8_HALF(fa[i], ks), acc[i][j], sa4[ks], sb4[ks]); \
+      }                                                                                           \
+    } else {                                                                                      \
+      _Pragma("unroll") for (int q = 0; q < TMA * TN; ++q) {                                      \
+        const int i = q / TN, j = q % TN;                                                         \
+        acc[i][j] = mfma8(i, j, fb[j], fa[i], acc[i][j], sa, sb);                                 \
+      }                                                                                           \
     }                                                                                             \
     mfma_fence(acc);                                                                              \
+  }
+#define GG8_PP_SCALES(P)                                                                          \
+  {                                                                                               \
+    if constexpr (FP4)                                                                            \
+      scale_load4(sa_tile, sb_tile, sc_bytes, P, sc + ((P) & 1) * kScaleSlot4, wave, lane);       \
+    else                                                                                          \
+      scale_load(sa_tile, sb_tile, sc_bytes, P, sc + ((P) & 1) * kScaleSlot, wave, lane);         \
   }
 #define GG8_PP_LOAD_B(U, Q)                                                                       \
   {                                                                                               \
@@ -1280,8 +1359,7 @@ __device__ __attribute__((always_inline)) inline void mainloop8_pp(
     GG8_PP_READ(((U) + 1) & 3)                                                                    \
     if (((U) & 1) == 0) GG8_PP_LOAD_B(U, (KT) + 4)                                                \
     else {                                                                                        \
-      scale_load(sa_tile, sb_tile, sc_bytes, ((KT) + 3) / 2, sc + ((((KT) + 3) / 2) & 1) * kScaleSlot, \
-                 wave, lane);                                                                     \
+      GG8_PP_SCALES(((KT) + 3) / 2)                                                               \
       GG8_PP_LOAD_A((U) == 1 ? a0 : a2, (KT) + 3)                                                 \
     }                                                                                             \
     __builtin_amdgcn_sched_barrier(0);                                                            \
@@ -1328,7 +1406,9 @@ __device__ __attribute__((always_inline)) inline void mainloop8_pp(
   }
 #undef GG8_PP_LOAD_A
 #undef GG8_PP_LOAD_B
+#undef GG8_PP_SCALES
 #undef GG8_PP_MFMA
+#undef GG8_HALF
 #undef GG8_PP_READ
 #undef GG8_RB
 #undef GG8_RA
@@ -1660,8 +1740,14 @@ __device__ __forceinline__ int half_tiles(int rows) {
 // mode, s_pref[0..E] with the exclusive prefix of the groups' full-height
 // row-tile counts and s_half[0..E] with that of their half-height last
 // tiles (0 or 1 per group).
+//
+// HalfCount: the type of s_half (16 bits are enough outside wgrad, and leave
+// fp4 room for its scales in LDS).
 template <int MODE>
-__device__ void decode_groups(const Params& p, int32_t* s_end, int32_t* s_pref, int32_t* s_half,
+using HalfCount = std::conditional_t<is_fp4(MODE), uint16_t, int32_t>;
+
+template <int MODE>
+__device__ void decode_groups(const Params& p, int32_t* s_end, int32_t* s_pref, HalfCount<MODE>* s_half,
                               int64_t* scratch, int tid) {
   const int E = p.num_groups;
   const int per = (E + NT - 1) / NT;
@@ -1705,7 +1791,7 @@ __device__ void decode_groups(const Params& p, int32_t* s_end, int32_t* s_pref, 
     int half = (int)((incl - local) >> 32);
     for (int g = g0; g < g1; ++g) {
       s_pref[g] = full;
-      s_half[g] = half;
+      s_half[g] = (HalfCount<MODE>)half;
       const int rows = s_end[g] - group_start<MODE>(s_end, g);
       const int h = half_tiles(rows);
       full += (rows + BM - 1) / BM - h;
@@ -1713,7 +1799,7 @@ __device__ void decode_groups(const Params& p, int32_t* s_end, int32_t* s_pref, 
     }
     if (tid == NT - 1) {
       s_pref[E] = (int)(incl & 0xffffffff);
-      s_half[E] = (int)(incl >> 32);
+      s_half[E] = (HalfCount<MODE>)(incl >> 32);
     }
     __syncthreads();
   } else if (E <= kOrderMaxGroups) {
@@ -1757,7 +1843,8 @@ __device__ void decode_groups(const Params& p, int32_t* s_end, int32_t* s_pref, 
 // Largest g in [0, E) with pref[g] <= t (pref is a non-decreasing
 // exclusive prefix, pref[0] = 0 <= t < pref[E]).  That group's count is
 // non-zero: pref[g] <= t < pref[g + 1].
-__device__ __forceinline__ int find_group(const int32_t* pref, int E, int t) {
+template <typename T>
+__device__ __forceinline__ int find_group(const T* pref, int E, int t) {
   int lo = 0, hi = E;          // invariant: pref[lo] <= t < pref[hi]
   while (hi - lo > 1) {
     int mid = (lo + hi) >> 1;
@@ -1831,20 +1918,23 @@ template <int MODE, bool OUT_F32, bool STAGED_F32 = false, bool WIDE = false>
 __global__ __launch_bounds__(NT, 1) void grouped_gemm_kernel(Params p) {
   static_assert(!WIDE || is_wgrad(MODE), "only wgrad reads an operand down a data-dependent span");
   constexpr bool A_STRIDED = is_wgrad(MODE);
-  constexpr bool B_STRIDED = !is_dgrad(MODE) && !is_fp8(MODE);
+  constexpr bool B_STRIDED = !is_dgrad(MODE) && !is_scaled(MODE);
   // Main loops: the bf16 row passes ping-pong with A in the pair layout,
   // wgrad ping-pongs with one stage per slot for both operands, the fp8
   // forward runs the row passes' schedule on bytes (mainloop8_pp).
-  constexpr bool PP_PAIR = !is_wgrad(MODE) && !is_fp8(MODE);
+  constexpr bool PP_PAIR = !is_wgrad(MODE) && !is_scaled(MODE);
 
   // LDS: NSTAGE stage buffers of 32 KB (A tile, then B tile); fp8: two
-  // k-blocks of scales.
+  // k-blocks of scales, fp4: two stage pairs of them (and the scan in them,
+  // which is done before they arrive).
   __shared__ __attribute__((aligned(16))) uint8_t smem[NSTAGE * STAGE_BYTES];
-  __shared__ __attribute__((aligned(16))) uint8_t s_sc[is_fp8(MODE) ? 2 * kScaleSlot : 16];
+  __shared__ __attribute__((aligned(16))) uint8_t s_sc[is_fp4(MODE) ? 2 * kScaleSlot4 : is_fp8(MODE) ? 2 * kScaleSlot : 16];
   __shared__ int32_t s_end[GG_MAX_GROUPS_DEV];
   __shared__ int32_t s_pref[GG_MAX_GROUPS_DEV + 1];
-  __shared__ int32_t s_half[GG_MAX_GROUPS_DEV + 1];
-  __shared__ int64_t s_scan[NT];
+  __shared__ HalfCount<MODE> s_half[GG_MAX_GROUPS_DEV + 1];
+  __shared__ int64_t s_scan_own[is_fp4(MODE) ? 1 : NT];
+  static_assert(2 * kScaleSlot4 >= NT * (int)sizeof(int64_t), "the scan fits the scale slots");
+  int64_t* const s_scan = is_fp4(MODE) ? reinterpret_cast<int64_t*>(s_sc) : s_scan_own;
 
   const int tid = threadIdx.x;
   const int lane = tid & 63;
@@ -1955,29 +2045,33 @@ __global__ __launch_bounds__(NT, 1) void grouped_gemm_kernel(Params p) {
       // full phase: row tile rt_all - s_pref[g] of group g; half phase:
       // the last row tile of group g
       const bool in_full = u < full_tiles;
-      const int g = uniform(find_group(in_full ? s_pref : s_half, E, (int)rt_all));
+      int found;
+      if constexpr (is_fp4(MODE)) found = in_full ? find_group(s_pref, E, (int)rt_all) : find_group(s_half, E, (int)rt_all);
+      else found = find_group(in_full ? s_pref : s_half, E, (int)rt_all);
+      const int g = uniform(found);
       const int s = uniform(group_start<MODE>(s_end, g)), e = uniform(s_end[g]);
       const int rt = in_full ? (int)rt_all - uniform(s_pref[g]) : (e - s - 1) / BM;
       const int row0 = s + rt * BM;             // first expert row of the tile
       const int rows = (e - row0) < BM ? (e - row0) : BM;
       const int64_t arow = is_masked(MODE) ? (int64_t)g * p.m + row0 : (int64_t)row0;
-      if constexpr (is_fp8(MODE)) {
+      if constexpr (is_scaled(MODE)) {
         // A(row i, red kk) = X[arow + i, kk];  B(row n, red kk) = W[g, col0 + n, kk]
-        // (one byte per value)
-        A.origin = pa + arow * p.k;
-        A.ld_bytes = (uint32_t)p.k;
+        // (one byte per value; fp4: per two, and all of it counted in bytes)
+        const int64_t kbytes = is_fp4(MODE) ? p.k / 2 : p.k;
+        A.origin = pa + arow * kbytes;
+        A.ld_bytes = (uint32_t)kbytes;
         A.rows = rows;
-        A.red = (int)p.k;
+        A.red = (int)kbytes;
         A.row_tail = 0;
-        B.origin = pb + ((int64_t)g * p.n + col0) * p.k;
-        B.ld_bytes = (uint32_t)p.k;
+        B.origin = pb + ((int64_t)g * p.n + col0) * kbytes;
+        B.ld_bytes = (uint32_t)kbytes;
         B.rows = (int)(p.n - col0 < BN ? p.n - col0 : BN);
-        B.red = (int)p.k;
+        B.red = (int)kbytes;
         B.row_tail = 0;
         T.ldc_bytes = (uint32_t)(esz * p.n);
         T.cbase = pc + esz * (arow * p.n + col0);
         // packed scale tiles: X row tile (experts in order), W column tile
-        const int64_t kblocks = p.k / 128;
+        const int64_t kblocks = scale_kblocks<MODE>(p.k);
         const int64_t xtile = is_masked(MODE) ? (int64_t)g * ((p.m + BM - 1) / BM) + rt
                                               : (int64_t)uniform(s_pref[g]) + uniform(s_half[g]) + rt;
         T.sa = p.sa + xtile * kblocks * 256;
@@ -2036,9 +2130,10 @@ __global__ __launch_bounds__(NT, 1) void grouped_gemm_kernel(Params p) {
       if constexpr (is_x8(MODE))
         prologue_loads_x8<WIDE>(sa0, sa1, sa2, T.A.origin, T.B.origin, T.sa, p.k / 128 * 256, T.sa_left, T.A, T.B,
                                 tid, wave, x8);
-      else if constexpr (is_fp8(MODE))
-        prologue_loads8_pp(sa0, sa1, sa2, sa0 + OP_BYTES, sa1 + OP_BYTES, sa2 + OP_BYTES, s_sc, T.A.origin,
-                           T.B.origin, T.sa, T.sb, (uint32_t)(p.k / 128 * 256), T.A, T.B, tid, wave);
+      else if constexpr (is_scaled(MODE))
+        prologue_loads8_pp<is_fp4(MODE)>(sa0, sa1, sa2, sa0 + OP_BYTES, sa1 + OP_BYTES, sa2 + OP_BYTES, s_sc,
+                                         T.A.origin, T.B.origin, T.sa, T.sb,
+                                         (uint32_t)(scale_kblocks<MODE>(p.k) * 256), T.A, T.B, tid, wave);
       else if constexpr (PP_PAIR)
         prologue_loads_pp_pair<B_STRIDED>(sa0, sa1, sa2, sa3, sa0 + OP_BYTES, sa1 + OP_BYTES, sa2 + OP_BYTES,
                                           T.A.origin, T.B.origin, T.A, T.B, tid, wave);
@@ -2077,16 +2172,16 @@ __global__ __launch_bounds__(NT, 1) void grouped_gemm_kernel(Params p) {
     if constexpr (is_x8(MODE)) {
       mainloop_x8<WIDE>(sa0, sa1, sa2, sa3, cur.A.origin, cur.B.origin, cur.sa, p.k / 128 * 256, cur.sa_left, cur.A,
                         cur.B, tid, wave, faa, fab, acc, x8);
-    } else if constexpr (is_fp8(MODE)) {
-      const uint32_t sc_bytes = (uint32_t)(p.k / 128 * 256);
+    } else if constexpr (is_scaled(MODE)) {
+      const uint32_t sc_bytes = (uint32_t)(scale_kblocks<MODE>(p.k) * 256);
       if (half)
-        mainloop8_pp<2>(sa0, sa1, sa2, sa3, sa0 + OP_BYTES, sa1 + OP_BYTES, sa2 + OP_BYTES, sa3 + OP_BYTES,
-                        s_sc, cur.A.origin, cur.B.origin, cur.sa, cur.sb, sc_bytes, cur.A, cur.B, tid, wave, wm,
-                        wn, 0, faa_half, fab, acc);
+        mainloop8_pp<2, is_fp4(MODE)>(sa0, sa1, sa2, sa3, sa0 + OP_BYTES, sa1 + OP_BYTES, sa2 + OP_BYTES,
+                                      sa3 + OP_BYTES, s_sc, cur.A.origin, cur.B.origin, cur.sa, cur.sb, sc_bytes,
+                                      cur.A, cur.B, tid, wave, wm, wn, 0, faa_half, fab, acc);
       else
-        mainloop8_pp<TM>(sa0, sa1, sa2, sa3, sa0 + OP_BYTES, sa1 + OP_BYTES, sa2 + OP_BYTES, sa3 + OP_BYTES,
-                         s_sc, cur.A.origin, cur.B.origin, cur.sa, cur.sb, sc_bytes, cur.A, cur.B, tid, wave, wm,
-                         wn, wm, faa, fab, acc);
+        mainloop8_pp<TM, is_fp4(MODE)>(sa0, sa1, sa2, sa3, sa0 + OP_BYTES, sa1 + OP_BYTES, sa2 + OP_BYTES,
+                                       sa3 + OP_BYTES, s_sc, cur.A.origin, cur.B.origin, cur.sa, cur.sb, sc_bytes,
+                                       cur.A, cur.B, tid, wave, wm, wn, wm, faa, fab, acc);
     } else if constexpr (PP_PAIR) {
       // the wave's A rows: 128 wm.. (full height, region wm) or 64 wm.. (half, region 0)
       if (half)
@@ -2108,7 +2203,7 @@ __global__ __launch_bounds__(NT, 1) void grouped_gemm_kernel(Params p) {
                                                     cur.B, tid, wave, faa, fab, acc, prev_stores);
     }
     const int64_t tn = t + gridDim.x;
-    if (OUT_F32 && !STAGED_F32 && !scaled && !is_silu(MODE) && !is_fp8(MODE)) {
+    if (OUT_F32 && !STAGED_F32 && !scaled && !is_silu(MODE) && !is_scaled(MODE)) {
       // Every wave is done reading this tile's stages: issue the next
       // tile's prologue loads first, then this tile's stores, so the
       // stores drain while those loads are in flight.  (Loads of stages
@@ -2162,7 +2257,7 @@ __global__ __launch_bounds__(NT, 1) void grouped_gemm_kernel(Params p) {
       } else if (is_x8(MODE) && whole_lines) {
         store_tile_lds<TM, OUT_F32, false, kNonTemporal>(cur.cbase, cur.ldc_bytes, cur.rows, cur.cols, wm, wn, lane,
                                                          acc, slab, 1.0f, 0.0f);
-      } else if constexpr (!OUT_F32 || is_fp8(MODE) || STAGED_F32) {
+      } else if constexpr (!OUT_F32 || is_scaled(MODE) || STAGED_F32) {
         if (half)
           store_tile_lds<2, OUT_F32, false>(cur.cbase, cur.ldc_bytes, cur.rows, cur.cols, wm, wn, lane,
                                             acc, slab, 1.0f, 0.0f);
@@ -2272,7 +2367,8 @@ hipError_t launch(int mode, const void* a, const void* b, const int32_t* groups,
 }
 
 
-hipError_t launch_fp8(bool masked, const void* x, const void* sx, const void* w, const void* sw,
+// fp8 and fp4 forward: modes FP8, FP8_MASKED, FP4, FP4_MASKED.
+static hipError_t launch_scaled(int mode, const void* x, const void* sx, const void* w, const void* sw,
                       const int32_t* groups, void* c, bool out_f32, int64_t m, int64_t k, int64_t n,
                       int32_t num_groups, int num_cus, hipStream_t stream) {
   Params p;
@@ -2290,12 +2386,30 @@ hipError_t launch_fp8(bool masked, const void* x, const void* sx, const void* w,
   p.sb = static_cast<const uint8_t*>(sw);
   p.bias = nullptr;
   p.bias_scale = nullptr;
-  const int mode = masked ? FP8_MASKED : FP8;
   const int64_t tiles = max_tiles(mode, m, k, n, num_groups);
   if (tiles <= 0) return hipSuccess;
   const int grid = (int)(tiles < num_cus ? tiles : num_cus);
-  return masked ? launch_mode<FP8_MASKED>(p, out_f32, grid, stream)
-                : launch_mode<FP8>(p, out_f32, grid, stream);
+  switch (mode) {
+    case FP8: return launch_mode<FP8>(p, out_f32, grid, stream);
+    case FP8_MASKED: return launch_mode<FP8_MASKED>(p, out_f32, grid, stream);
+    case FP4: return launch_mode<FP4>(p, out_f32, grid, stream);
+    case FP4_MASKED: return launch_mode<FP4_MASKED>(p, out_f32, grid, stream);
+  }
+  return hipErrorInvalidValue;
+}
+
+hipError_t launch_fp8(bool masked, const void* x, const void* sx, const void* w, const void* sw,
+                      const int32_t* groups, void* c, bool out_f32, int64_t m, int64_t k, int64_t n,
+                      int32_t num_groups, int num_cus, hipStream_t stream) {
+  return launch_scaled(masked ? FP8_MASKED : FP8, x, sx, w, sw, groups, c, out_f32, m, k, n, num_groups, num_cus,
+                       stream);
+}
+
+hipError_t launch_fp4(bool masked, const void* x, const void* sx, const void* w, const void* sw,
+                      const int32_t* groups, void* c, bool out_f32, int64_t m, int64_t k, int64_t n,
+                      int32_t num_groups, int num_cus, hipStream_t stream) {
+  return launch_scaled(masked ? FP4_MASKED : FP4, x, sx, w, sw, groups, c, out_f32, m, k, n, num_groups, num_cus,
+                       stream);
 }
 
 hipError_t launch_fp8_wgrad(bool masked, const void* x, const void* sx, const void* dy, const int32_t* groups,
