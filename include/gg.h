@@ -802,6 +802,59 @@ gg_status gg_fp4_masked_forward(const void* x, const void* x_scales,
                                 gg_dtype y_dtype, int64_t max_m, int64_t k,
                                 int64_t n, int32_t num_groups, void* stream);
 
+/*
+ * The expert layer for a few tokens
+ * ---------------------------------
+ * A decoding step's whole layer in two kernels, without routing, gather and
+ * tiles that are nearly empty:
+ *   out[t] = sum_s weights[t, s] W2[e] (silu(W1[e] x[t]) * (W3[e] x[t])),
+ *   e = expert_of_slot[t * topk + s]
+ * what gg_route, gg_gather_rows, gg_forward_nk, gg_silu_mul_rows, gg_forward_nk
+ * and gg_combine_rows give together.
+ *   x        [tokens, hidden]        bf16
+ *   expert_of_slot  int32 [tokens, topk]; values outside [0, num_groups) drop
+ *            the slot.  A token without slots gets zeros; one that names an
+ *            expert twice gets it with the sum of both weights
+ *   weights  fp32 [tokens, topk], or NULL for 1
+ *   w13      [E, 2 inter, hidden]    the rows of W1 (gate), then of W3 (up)
+ *   w2       [E, hidden, inter]
+ *   out      [tokens, hidden]        out_dtype
+ *   workspace  gg_moe_few_tokens_workspace_bytes(tokens, topk, inter,
+ *            num_groups) bytes of device memory, 16-byte aligned, the caller's;
+ *            its contents on entry do not matter.  Calls that may overlap (two
+ *            captured graphs among them) need one each.
+ * gg_moe_few_tokens takes bf16 weights, hidden and inter multiples of 8;
+ * gg_fp4_moe_few_tokens takes e2m1 codes [.., k / 2] with packed scales
+ * (GG_FP4_WEIGHT), hidden and inter multiples of 32; the activations stay bf16.
+ * Sums are fp32 in a fixed order; weights[t, s] silu(.) (.) is rounded to bf16
+ * once on the way, out once at the end.  An infinity or NaN of an expert's
+ * weights reaches its own tokens only.
+ * tokens <= GG_FEW_TOKENS_MAX and tokens * topk <= GG_FEW_SLOTS_MAX
+ * (GG_ERR_LIMIT otherwise), and 2 * inter * hidden < 2^31.  No expert that no
+ * token chose is read.  Errors otherwise as the GEMM entry points; safe to capture
+ * in a HIP graph.
+ * Cited passage: sglang PR #32385, "Cause" (the decoding step's gate/up, SiLU-mul
+ * and down products over a few rows of each expert).
+ */
+#define GG_FEW_TOKENS_MAX 64
+#define GG_FEW_SLOTS_MAX 1024
+int64_t gg_moe_few_tokens_workspace_bytes(int64_t tokens, int32_t topk,
+                                          int64_t inter, int32_t num_groups);
+gg_status gg_moe_few_tokens(const void* x, const int32_t* expert_of_slot,
+                            const float* weights, const void* w13,
+                            const void* w2, void* out, gg_dtype out_dtype,
+                            void* workspace, int64_t tokens, int32_t topk,
+                            int64_t hidden, int64_t inter, int32_t num_groups,
+                            void* stream);
+gg_status gg_fp4_moe_few_tokens(const void* x, const int32_t* expert_of_slot,
+                                const float* weights, const void* w13,
+                                const void* w13_scales, const void* w2,
+                                const void* w2_scales, void* out,
+                                gg_dtype out_dtype, void* workspace,
+                                int64_t tokens, int32_t topk, int64_t hidden,
+                                int64_t inter, int32_t num_groups,
+                                void* stream);
+
 /* Static description of a status code. */
 const char* gg_status_str(gg_status s);
 

@@ -133,9 +133,14 @@ def load():
                        ("gg_fp4_masked_silu_mul_rows", [P, P, P, P, I64, I64, I32, P]),
                        ("gg_fp4_dequantize", [ctypes.c_int, P, P, P, I64, I64, I32, P, P]),
                        ("gg_fp4_forward", [P, P, P, P, P, P, ctypes.c_int, I64, I64, I64, I32, P]),
-                       ("gg_fp4_masked_forward", [P, P, P, P, P, P, ctypes.c_int, I64, I64, I64, I32, P])):
+                       ("gg_fp4_masked_forward", [P, P, P, P, P, P, ctypes.c_int, I64, I64, I64, I32, P]),
+                       ("gg_moe_few_tokens", [P, P, P, P, P, P, ctypes.c_int, P, I64, I32, I64, I64, I32, P]),
+                       ("gg_fp4_moe_few_tokens",
+                        [P, P, P, P, P, P, P, P, ctypes.c_int, P, I64, I32, I64, I64, I32, P])):
         getattr(lib, name).argtypes = args
         getattr(lib, name).restype = ctypes.c_int
+    lib.gg_moe_few_tokens_workspace_bytes.argtypes = [I64, I32, I64, I32]
+    lib.gg_moe_few_tokens_workspace_bytes.restype = ctypes.c_int64
     lib.gg_status_str.argtypes = [ctypes.c_int]
     lib.gg_status_str.restype = ctypes.c_char_p
     lib.gg_last_error.argtypes = []
@@ -1235,3 +1240,75 @@ def fp4_masked_forward(x, x_scales, w, w_scales, masked_m, out=None, out_dtype=N
     """The masked 4-bit forward (gg_fp4_masked_forward): x uint8 [E, max_m,
     k / 2], x_scales packed with GG_FP4_ACT_MASKED and the same masked_m."""
     return _fp4_forward("gg_fp4_masked_forward", GG_FP4_ACT_MASKED, x, x_scales, w, w_scales, masked_m, out, out_dtype)
+
+
+# ---------------------------------------------------------------------------
+# the expert layer for a few tokens
+# ---------------------------------------------------------------------------
+
+FEW_TOKENS_MAX = 64
+FEW_SLOTS_MAX = 1024
+
+
+def moe_few_tokens_workspace_bytes(tokens, topk, inter, num_groups) -> int:
+    v = int(load().gg_moe_few_tokens_workspace_bytes(int(tokens), int(topk), int(inter), int(num_groups)))
+    if v < 0:
+        raise ValueError("invalid arguments for gg_moe_few_tokens_workspace_bytes")
+    return v
+
+
+def _few_tokens(name, x, experts, weights, w13, s13, w2, s2, wdtype, per, out, out_dtype, workspace):
+    torch = _torch()
+    dev = x.device
+    _check(x, "x", torch.bfloat16, 2, dev)
+    tokens, hidden = x.shape
+    _check(experts, "experts", torch.int32, 2, dev)
+    if experts.shape[0] != tokens:
+        raise ValueError("experts must be [tokens, topk]")
+    topk = experts.shape[1]
+    if weights is not None:
+        _shaped(weights, "weights", torch.float32, (tokens, topk), dev)
+    _check(w13, "w13", wdtype, 3, dev)
+    _check(w2, "w2", wdtype, 3, dev)
+    e, inter = w13.shape[0], w13.shape[1] // 2
+    if w13.shape[1] % 2 or w13.shape[2] * per != hidden or w2.shape[0] != e or w2.shape[1] != hidden or \
+            w2.shape[2] * per != inter:
+        raise ValueError("shape mismatch between x, w13 and w2")
+    if per == 2:
+        if hidden % 32 or inter % 32:
+            raise ValueError("hidden and inter must be multiples of 32")
+        if s13 is None or s2 is None:
+            raise ValueError("w13_scales and w2_scales are required")
+        _packed4(s13, "w13_scales", GG_FP4_WEIGHT, 2 * inter, hidden, e, dev)
+        _packed4(s2, "w2_scales", GG_FP4_WEIGHT, hidden, inter, e, dev)
+    need = moe_few_tokens_workspace_bytes(tokens, topk, inter, e)
+    if workspace is None:
+        workspace = _shaped(None, "workspace", torch.uint8, (need,), dev)
+    _check(workspace, "workspace", torch.uint8, 1, dev)
+    if workspace.numel() < need:
+        raise ValueError(f"workspace must hold {need} bytes")
+    out = _shaped(out, "out", (out_dtype or torch.bfloat16) if out is None else out.dtype, (tokens, hidden), dev)
+    ws = (_ptr(w13), _ptr(s13), _ptr(w2), _ptr(s2)) if per == 2 else (_ptr(w13), _ptr(w2))
+    _launch(name, dev, _ptr(x), _ptr(experts), _ptr(weights), *ws, _ptr(out), _dtype_code(out.dtype), _ptr(workspace),
+            tokens, topk, hidden, inter, e)
+    return out
+
+
+def moe_few_tokens(x, experts, w13, w2, weights=None, out=None, out_dtype=None, workspace=None):
+    """The expert layer for up to 64 tokens (gg_moe_few_tokens): x bf16
+    [tokens, hidden]; experts int32 [tokens, topk] (out of range: dropped);
+    w13 bf16 [E, 2I, hidden] (gate rows first), w2 bf16 [E, hidden, I];
+    weights fp32 [tokens, topk] or None for 1.  Returns [tokens, hidden]."""
+    torch = _torch()
+    return _few_tokens("gg_moe_few_tokens", x, experts, weights, w13, None, w2, None, torch.bfloat16, 1, out, out_dtype,
+                       workspace)
+
+
+def fp4_moe_few_tokens(x, experts, w13, w13_scales, w2, w2_scales, weights=None, out=None, out_dtype=None,
+                       workspace=None):
+    """moe_few_tokens with 4-bit weights (gg_fp4_moe_few_tokens): w13 uint8
+    [E, 2I, hidden / 2], w2 uint8 [E, hidden, I / 2] with their packed scales
+    (GG_FP4_WEIGHT), as ``fp4_forward`` takes them."""
+    torch = _torch()
+    return _few_tokens("gg_fp4_moe_few_tokens", x, experts, weights, w13, w13_scales, w2, w2_scales, torch.uint8, 2, out,
+                       out_dtype, workspace)

@@ -14,7 +14,7 @@ CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libgg.so")
 SOURCES = ["gg_kernels.hip", "gg_fp8_scales.hip", "gg_route.hip", "gg_bias_grad.hip", "gg_norm.hip",
            "gg_fp8_gather.hip", "gg_combine_grad.hip", "gg_silu_rows.hip",
-           "gg_fp4_rows.hip", "gg_api.hip"]
+           "gg_fp4_rows.hip", "gg_few_tokens.hip", "gg_api.hip"]
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950",

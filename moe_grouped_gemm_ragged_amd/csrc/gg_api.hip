@@ -916,6 +916,58 @@ gg_status gg_fp4_masked_forward(const void* x, const void* x_scales, const void*
   return fp4_run(true, x, x_scales, w, w_scales, masked_m, y, y_dtype, max_m, k, n, num_groups, stream);
 }
 
+// ---- the expert layer for a few tokens ---------------------------------------------------
+
+static_assert(GG_FEW_TOKENS_MAX == gg::kFewTokensMax && GG_FEW_SLOTS_MAX == gg::kFewSlotsMax, "limits differ");
+
+int64_t gg_moe_few_tokens_workspace_bytes(int64_t tokens, int32_t topk, int64_t inter, int32_t num_groups) {
+  if (tokens < 0 || tokens > GG_FEW_TOKENS_MAX || topk < 1 || tokens * (int64_t)topk > GG_FEW_SLOTS_MAX) return -1;
+  if (inter < 8 || inter % 8 != 0 || inter > GG_MAX_KN || num_groups < 1 || num_groups > GG_MAX_GROUPS) return -1;
+  return gg::few_tokens_workspace(tokens * topk, inter, num_groups);
+}
+
+static gg_status few_run(bool four, const void* x, const int32_t* experts, const float* weights, const void* w13,
+                         const void* s13, const void* w2, const void* s2, void* out, gg_dtype out_dtype,
+                         void* workspace, int64_t tokens, int32_t topk, int64_t hidden, int64_t inter, int32_t E,
+                         void* stream) {
+  if (!w13 || !w2 || (four && (!s13 || !s2)) || (tokens > 0 && (!x || !experts || !out || !workspace)))
+    return fail(GG_ERR_NULL_PTR, "a required pointer is NULL");
+  if (out_dtype != GG_BF16 && out_dtype != GG_F32)
+    return fail(GG_ERR_BAD_DTYPE, "output dtype must be GG_BF16 or GG_F32");
+  if (E < 1 || E > GG_MAX_GROUPS) return fail(GG_ERR_LIMIT, "num_groups must be in [1, GG_MAX_GROUPS]");
+  const int64_t step = four ? 32 : 8;
+  if (tokens < 0 || topk < 1 || hidden < step || inter < step || hidden % step != 0 || inter % step != 0)
+    return fail(GG_ERR_BAD_DIM, four ? "need tokens >= 0, topk >= 1, hidden and inter positive multiples of 32"
+                                     : "need tokens >= 0, topk >= 1, hidden and inter positive multiples of 8");
+  if (hidden > GG_MAX_KN || 2 * inter > GG_MAX_KN)
+    return fail(GG_ERR_BAD_DIM, "hidden and 2 * inter must not exceed GG_MAX_KN");
+  if (tokens > GG_FEW_TOKENS_MAX || tokens * (int64_t)topk > GG_FEW_SLOTS_MAX)
+    return fail(GG_ERR_LIMIT, "need tokens <= GG_FEW_TOKENS_MAX and tokens * topk <= GG_FEW_SLOTS_MAX");
+  if (2 * inter * hidden >= (int64_t(1) << 31))
+    return fail(GG_ERR_BAD_DIM, "2 * inter * hidden must be below 2^31");
+  if (!aligned16(x) || !aligned16(w13) || !aligned16(w2) || !aligned16(s13) || !aligned16(s2) || !aligned16(out) ||
+      !aligned16(workspace) || !aligned4(experts) || !aligned4(weights))
+    return fail(GG_ERR_ALIGNMENT, "pointers must be 16-byte aligned, int32 and fp32 arrays 4-byte aligned");
+  return hip_result(gg::launch_few_tokens(four, x, experts, weights, w13, s13, w2, s2, out, out_dtype == GG_F32,
+                                          workspace, tokens, topk, hidden, inter, E,
+                                          static_cast<hipStream_t>(stream)));
+}
+
+gg_status gg_moe_few_tokens(const void* x, const int32_t* expert_of_slot, const float* weights, const void* w13,
+                            const void* w2, void* out, gg_dtype out_dtype, void* workspace, int64_t tokens,
+                            int32_t topk, int64_t hidden, int64_t inter, int32_t num_groups, void* stream) {
+  return few_run(false, x, expert_of_slot, weights, w13, nullptr, w2, nullptr, out, out_dtype, workspace, tokens, topk,
+                 hidden, inter, num_groups, stream);
+}
+
+gg_status gg_fp4_moe_few_tokens(const void* x, const int32_t* expert_of_slot, const float* weights, const void* w13,
+                                const void* w13_scales, const void* w2, const void* w2_scales, void* out,
+                                gg_dtype out_dtype, void* workspace, int64_t tokens, int32_t topk, int64_t hidden,
+                                int64_t inter, int32_t num_groups, void* stream) {
+  return few_run(true, x, expert_of_slot, weights, w13, w13_scales, w2, w2_scales, out, out_dtype, workspace, tokens,
+                 topk, hidden, inter, num_groups, stream);
+}
+
 const char* gg_status_str(gg_status s) {
   switch (s) {
     case GG_OK: return "GG_OK";

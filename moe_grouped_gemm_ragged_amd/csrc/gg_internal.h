@@ -75,6 +75,17 @@ hipError_t launch_fp4_dequantize(int layout, const void* codes, const void* scal
 hipError_t launch_fp4_pack_scales(int layout, const void* src, int64_t ld_src, const int32_t* groups, int64_t rows,
                                   int64_t k, int32_t E, void* dst, int num_cus, hipStream_t stream);
 
+// The expert layer for a few tokens (gg_few_tokens.hip): w13 [E, 2 inter,
+// hidden] and w2 [E, hidden, inter] in bf16, or codes with packed scales.  share
+// may be null.  tokens <= kFewTokensMax, tokens * topk <= kFewSlotsMax.
+constexpr int kFewTokensMax = 64;
+constexpr int kFewSlotsMax = 1024;
+int64_t few_tokens_workspace(int64_t slots, int64_t inter, int32_t E);
+hipError_t launch_few_tokens(bool four, const void* x, const int32_t* experts, const float* share, const void* w13,
+                             const void* s13, const void* w2, const void* s2, void* out, bool out_f32, void* workspace,
+                             int64_t tokens, int32_t topk, int64_t hidden, int64_t inter, int32_t E,
+                             hipStream_t stream);
+
 // The weight gradient from e4m3 activations: x [rows, k] e4m3 with scales sx
 // in the packed layout, dy bf16, dw[g] = alpha * x^T dy + beta * dw[g].
 // Arguments were validated by the caller.
