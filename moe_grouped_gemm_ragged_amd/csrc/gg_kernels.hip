@@ -1265,14 +1265,25 @@ __device__ __attribute__((always_inline)) inline void prologue_loads8_pp(
   }
 }
 
-template <int TMA, bool FP4>
+// fp4 tiles start with the previous tile's `prev_stores` stores in flight
+// (issued after this tile's prologue loads): 0, STORES (a tile of full height)
+// or half of that.  The waits for prologue loads leave them in flight: group
+// 0's until it reads stage 4, group 1's until stage 2.
+template <int N, int STORES>
+__device__ __forceinline__ void pp_sync_past(const Regions& rg, int prev_stores) {
+  if (STORES > 0 && prev_stores == STORES) pp_sync<N + STORES>(rg);
+  else if (STORES > 0 && prev_stores == STORES / 2) pp_sync<N + STORES / 2>(rg);
+  else pp_sync<N>(rg);
+}
+
+template <int TMA, bool FP4, int STORES>
 __device__ __attribute__((always_inline)) inline void mainloop8_pp(
     uint8_t* __restrict__ a0, uint8_t* __restrict__ a1, uint8_t* __restrict__ a2, uint8_t* __restrict__ a3,
     uint8_t* __restrict__ b0, uint8_t* __restrict__ b1, uint8_t* __restrict__ b2, uint8_t* __restrict__ b3,
     uint8_t* __restrict__ sc, const uint8_t* __restrict__ a_origin, const uint8_t* __restrict__ b_origin,
     const uint8_t* __restrict__ sa_tile, const uint8_t* __restrict__ sb_tile, uint32_t sc_bytes, Operand A,
     Operand B, int tid, int wave, int wm, int wn, int ha, const FragAddr& faa, const FragAddr& fab,
-    floatx16 (&acc)[TM][TN]) {
+    floatx16 (&acc)[TM][TN], [[maybe_unused]] int prev_stores) {
   A.origin = a_origin;
   B.origin = b_origin;
   // even: K is a multiple of 128 (fp8), or a last pair's second stage is
@@ -1291,7 +1302,7 @@ __device__ __attribute__((always_inline)) inline void mainloop8_pp(
   u32x2 sa4 = {0u, 0u}, sb4 = {0u, 0u};
   // group 0: the scales, B of stage 0 and its half of A pair 0 landed (the
   // last 8 loads may be in flight); group 1 waits at the next barrier
-  if (g0) pp_sync<8>(rg); else pp_sync<kNoVm>(rg);
+  if (g0) pp_sync_past<8, STORES>(rg, prev_stores); else pp_sync<kNoVm>(rg);
 
 #define GG8_RA(U) ((U) < 2 ? (ha ? a1 : a0) : (ha ? a3 : a2))
 #define GG8_RB(U) ((U) == 0 ? b0 : (U) == 1 ? b1 : (U) == 2 ? b2 : b3)
@@ -1354,7 +1365,8 @@ __device__ __attribute__((always_inline)) inline void mainloop8_pp(
     __builtin_amdgcn_sched_barrier(0);                                                            \
     GG8_PP_MFMA()                                                                                 \
     __builtin_amdgcn_sched_barrier(0);                                                            \
-    if ((U) & 1) pp_sync<4>(rg); else pp_sync<kNoVm>(rg);                                          \
+    if (FP4 && (U) == 1 && (KT) == 1) pp_sync_past<4, STORES>(rg, prev_stores);                    \
+    else if ((U) & 1) pp_sync<4>(rg); else pp_sync<kNoVm>(rg);                                     \
     __builtin_amdgcn_sched_barrier(0);                                                            \
     GG8_PP_READ(((U) + 1) & 3)                                                                    \
     if (((U) & 1) == 0) GG8_PP_LOAD_B(U, (KT) + 4)                                                \
@@ -1377,7 +1389,7 @@ __device__ __attribute__((always_inline)) inline void mainloop8_pp(
   } else {
     // this group's half of A pair 0 landed (B of stage 1 may be in flight)
     __builtin_amdgcn_sched_barrier(0);
-    pp_sync<4>(rg);
+    pp_sync_past<4, STORES>(rg, prev_stores);
     // stage KT = kt + U: read it and load (U even) this group's half of the A
     // pair of stages KT + 2, KT + 3 into slot (U + 3) mod 4 or (U odd) B of
     // stage KT + 2 into slot (U + 2) mod 4; then compute it
@@ -1388,7 +1400,8 @@ __device__ __attribute__((always_inline)) inline void mainloop8_pp(
     if (((U) & 1) == 0) GG8_PP_LOAD_A((U) == 0 ? a3 : a1, (KT) + 2)                               \
     else GG8_PP_LOAD_B(((U) + 2) & 3, (KT) + 2)                                                   \
     __builtin_amdgcn_sched_barrier(0);                                                            \
-    if (((U) & 1) == 0) pp_sync<4>(rg); else pp_sync<kNoVm>(rg);                                   \
+    if (FP4 && (U) == 0 && (KT) == 0) pp_sync_past<4, STORES>(rg, prev_stores);                    \
+    else if (((U) & 1) == 0) pp_sync<4>(rg); else pp_sync<kNoVm>(rg);                                   \
     __builtin_amdgcn_sched_barrier(0);                                                            \
     GG8_PP_MFMA()                                                                                 \
     __builtin_amdgcn_sched_barrier(0);                                                            \
@@ -1631,6 +1644,82 @@ __device__ __forceinline__ void store_tile_x8(uint8_t* cbase, uint32_t ldc_bytes
   }
 }
 
+// The fp4 epilogue.  A tile's stores are acknowledged at memory's pace, and a
+// wave's loads wait behind them in the order of issue: with the next tile's
+// first loads issued after the stores, a tile began when the last one's output
+// had left the chip's caches.  So those loads go first, into slots 0 to 2, and
+// the output passes through slot 3, 4 KB a wave: 32 rows of 64 columns already
+// rounded to bf16, or 32 of fp32.
+//
+// bf16: row r, column group of 4 values g (8 bytes) at 8 (g ^ (r / 2 mod 16)),
+// so that the 32 rows that a write touches cover all banks; a read takes two
+// neighbouring groups, swapped where r / 2 is odd.  fp32: chunk c of 4 values at
+// 16 (c ^ (r / 2 mod 8)).
+template <int TMA, bool OUT_F32>
+constexpr int stores_early() { return OUT_F32 ? TMA * TN * 4 : TMA * 4; }
+
+//
+// NT: non-temporal stores where rows begin on cache lines (store_tile_x8's
+// rule): 32 experts of 2048 rows, n 2048, bf16: k 512 99.0 -> 89.9 us, k 2048
+// 189 -> 172; 512 rows each, whose output the caches hold, within 6 % either way.
+template <int TMA, bool OUT_F32, bool NT>
+__device__ __forceinline__ void store_tile_early(uint8_t* cbase, uint32_t ldc_bytes, int rows, int cols, int wm, int wn,
+                                                 int lane, floatx16 (&acc)[TM][TN], uint8_t* slab) {
+  constexpr uint32_t esz = OUT_F32 ? 4 : 2;
+  const uint32_t nrec = (uint32_t)(rows - 1) * ldc_bytes + (uint32_t)cols * esz;
+  const __amdgpu_buffer_rsrc_t rs = make_rsrc(cbase, nrec);
+  const uint32_t l = opaque_v((uint32_t)lane);
+  const uint32_t wrow = l & 31u, half = l >> 5;            // written: this row, column groups 8 (..) + 4 half
+  const uint32_t rrow = l >> 3, rchunk = l & 7u;           // read: rows rrow + 8 q, chunk rchunk
+  const uint32_t row_off = (uint32_t)(32 * TMA * wm) * ldc_bytes + rrow * ldc_bytes;
+#pragma unroll
+  for (int i = 0; i < TMA; ++i) {
+    if constexpr (OUT_F32) {
+#pragma unroll
+      for (int j = 0; j < TN; ++j) {
+        asm volatile("" : "+a"(acc[i][j]));
+#pragma unroll
+        for (int rr = 0; rr < 4; ++rr) {
+          floatx4 v = {acc[i][j][4 * rr + 0], acc[i][j][4 * rr + 1], acc[i][j][4 * rr + 2], acc[i][j][4 * rr + 3]};
+          *reinterpret_cast<floatx4*>(slab + 128 * wrow + 16 * (((uint32_t)(2 * rr) + half) ^ (wrow >> 1 & 7u))) = v;
+        }
+        const int gcol = 64 * wn + 32 * j + 4 * (int)rchunk;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const uint32_t r = rrow + (uint32_t)(8 * q);
+          const floatx4 v = *reinterpret_cast<const floatx4*>(slab + 128 * r + 16 * (rchunk ^ (r >> 1 & 7u)));
+          const uint32_t off = gcol < cols ? row_off + (uint32_t)(32 * i + 8 * q) * ldc_bytes + (uint32_t)gcol * 4u
+                                           : kOutOfRange;
+          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), rs, off, 0, NT ? kNonTemporal : 0);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < TN; ++j) {
+        // (keeps the block in accumulator registers up to here)
+        asm volatile("" : "+a"(acc[i][j]));
+#pragma unroll
+        for (int rr = 0; rr < 4; ++rr) {
+          const u32x2 v = {pack_bf16x2(acc[i][j][4 * rr + 0], acc[i][j][4 * rr + 1]),
+                           pack_bf16x2(acc[i][j][4 * rr + 2], acc[i][j][4 * rr + 3])};
+          *reinterpret_cast<u32x2*>(slab + 128 * wrow + 8 * (((uint32_t)(8 * j + 2 * rr) + half) ^ (wrow >> 1))) = v;
+        }
+      }
+      const int gcol = 64 * wn + 8 * (int)rchunk;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const uint32_t r = rrow + (uint32_t)(8 * q);
+        const u32x4 v = *reinterpret_cast<const u32x4*>(slab + 128 * r + 16 * (rchunk ^ (r >> 2)));
+        const bool swap = (rrow >> 1 & 1u) != 0u;
+        const u32x4 o = {swap ? v[2] : v[0], swap ? v[3] : v[1], swap ? v[0] : v[2], swap ? v[1] : v[3]};
+        const uint32_t off = gcol < cols ? row_off + (uint32_t)(32 * i + 8 * q) * ldc_bytes + (uint32_t)gcol * 2u
+                                         : kOutOfRange;
+        __builtin_amdgcn_raw_buffer_store_b128(o, rs, off, 0, NT ? kNonTemporal : 0);
+      }
+    }
+  }
+}
+
 // The SiLU-mul epilogue of a gate/up tile: waves 0, 1 (mod 4) hold the gate
 // columns 64 wn .. of the tile's 128 activation columns and waves 2, 3 the
 // matching up columns, so the two halves meet in LDS.  Per block row every
@@ -1840,17 +1929,102 @@ __device__ void decode_groups(const Params& p, int32_t* s_end, int32_t* s_pref, 
   }
 }
 
+// The same for the fp4 modes, whose tiles are short enough for its time to
+// count: scans by lane exchanges within a wave, the waves joined once (a block
+// scan takes 18 barriers).
+template <bool MAX, typename T>
+__device__ __forceinline__ T wave_scan_incl(T v, int lane) {
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const T o = __shfl_up(v, (unsigned)d, 64);
+    if (lane >= d) v = MAX ? (v > o ? v : o) : v + o;
+  }
+  return v;
+}
+
+template <int MODE>
+__device__ void decode_groups4(const Params& p, int32_t* s_end, int32_t* s_pref, HalfCount<MODE>* s_half,
+                               int64_t* scratch, int tid) {
+  const int E = p.num_groups;
+  const int lane = tid & 63, wave = tid >> 6;
+  const int per = (E + NT - 1) / NT;
+  const int g0 = tid * per;
+  const int g1 = g0 + per < E ? g0 + per : E;
+  if constexpr (is_masked(MODE)) {
+    for (int g = g0; g < g1; ++g) {
+      int a = p.groups[g];
+      a = a < 0 ? 0 : a;
+      s_end[g] = a > p.m ? (int)p.m : a;
+    }
+  } else {
+    int run = 0;
+    for (int g = g0; g < g1; ++g) {
+      const int o = p.groups[g];
+      run = o > run ? o : run;
+      s_end[g] = run;
+    }
+    const int incl = wave_scan_incl<true>(run, lane);
+    if (lane == 63) scratch[wave] = incl;
+    __syncthreads();
+    int before = __shfl_up(incl, 1u, 64);
+    if (lane == 0) before = 0;
+    for (int w = 0; w < wave; ++w) before = (int)scratch[w] > before ? (int)scratch[w] : before;
+    for (int g = g0; g < g1; ++g) {
+      const int e = s_end[g] > before ? s_end[g] : before;
+      s_end[g] = e < (int)p.m ? e : (int)p.m;
+    }
+  }
+  __syncthreads();
+  // (full, half) counts packed as in decode_groups
+  int64_t local = 0;
+  for (int g = g0; g < g1; ++g) {
+    const int rows = s_end[g] - group_start<MODE>(s_end, g);
+    const int h = half_tiles(rows);
+    local += (int64_t)((rows + BM - 1) / BM - h) + ((int64_t)h << 32);
+  }
+  const int64_t incl = wave_scan_incl<false>(local, lane);
+  if (lane == 63) scratch[NWAVE + wave] = incl;
+  __syncthreads();
+  int64_t before = incl - local;
+  for (int w = 0; w < wave; ++w) before += scratch[NWAVE + w];
+  int full = (int)(before & 0xffffffff), half = (int)(before >> 32);
+  for (int g = g0; g < g1; ++g) {
+    s_pref[g] = full;
+    s_half[g] = (HalfCount<MODE>)half;
+    const int rows = s_end[g] - group_start<MODE>(s_end, g);
+    const int h = half_tiles(rows);
+    full += (rows + BM - 1) / BM - h;
+    half += h;
+  }
+  if (tid == NT - 1) {
+    s_pref[E] = full;
+    s_half[E] = (HalfCount<MODE>)half;
+  }
+  __syncthreads();
+}
+
 // Largest g in [0, E) with pref[g] <= t (pref is a non-decreasing
 // exclusive prefix, pref[0] = 0 <= t < pref[E]).  That group's count is
 // non-zero: pref[g] <= t < pref[g + 1].
-template <typename T>
-__device__ __forceinline__ int find_group(const T* pref, int E, int t) {
+__device__ __forceinline__ int find_group(const int32_t* pref, int E, int t) {
   int lo = 0, hi = E;          // invariant: pref[lo] <= t < pref[hi]
   while (hi - lo > 1) {
     int mid = (lo + hi) >> 1;
     if (pref[mid] <= t) lo = mid; else hi = mid;
   }
   return lo;
+}
+
+// The same by the whole wave at once (fp4): two looks, at every 64th part's
+// first entry and within the part, instead of one for each halving.
+template <typename T>
+__device__ __forceinline__ int find_group_wave(const T* pref, int E, int t, int lane) {
+  const int part = (E + 63) >> 6;
+  const int i = lane * part;
+  const int at = (__popcll(__ballot(i < E && (int)pref[i < E ? i : 0] <= t)) - 1) * part;
+  const int k = at + lane;
+  const bool in = lane < part && k < E;
+  return at + __popcll(__ballot(in && (int)pref[in ? k : 0] <= t)) - 1;
 }
 
 // ---- tile order -------------------------------------------------------------------
@@ -1943,7 +2117,8 @@ __global__ __launch_bounds__(NT, 1) void grouped_gemm_kernel(Params p) {
   const int wn = wave & 3;
   const int E = p.num_groups;
 
-  decode_groups<MODE>(p, s_end, s_pref, s_half, s_scan, tid);
+  if constexpr (is_fp4(MODE)) decode_groups4<MODE>(p, s_end, s_pref, s_half, s_scan, tid);
+  else decode_groups<MODE>(p, s_end, s_pref, s_half, s_scan, tid);
 
   // Output tile grid.  A SiLU tile writes 128 activation columns from a
   // 256-column panel: 128 gate columns and the 128 matching up columns.
@@ -1979,6 +2154,65 @@ __global__ __launch_bounds__(NT, 1) void grouped_gemm_kernel(Params p) {
   uint8_t* const sa1 = smem + STAGE_BYTES;
   uint8_t* const sa2 = smem + 2 * STAGE_BYTES;
   uint8_t* const sa3 = smem + 3 * STAGE_BYTES;
+
+  // fp4 tiles are found ahead of their use, with divisions of 32 bits (the grid
+  // then has fewer tiles than that, or the long way is taken).
+  struct Place {
+    int g, ct, rt, row0, rows;
+  };
+  auto locate = [&](int64_t t) __attribute__((always_inline)) {
+    const int64_t u = xcd_tile(t, total, false);
+    const bool in_full = u < full_tiles;
+    const int64_t v = in_full ? u : u - full_tiles;
+    const int row_tiles = uniform(in_full ? s_pref[E] : (int)s_half[E]);
+    int rt_all, ct;
+    if (total < (int64_t(1) << 31)) {
+      // strip_order
+      const uint32_t bw = col_tiles < kStrip ? col_tiles : kStrip, per = (uint32_t)row_tiles * bw, w0 = (uint32_t)v;
+      const uint32_t s = w0 / per, left = (uint32_t)col_tiles - s * bw, width = left < bw ? left : bw;
+      const uint32_t w = w0 - s * per, r = w / width;
+      rt_all = (int)r;
+      ct = (int)(s * bw + (w - r * width));
+    } else {
+      int64_t r;
+      strip_order(v, row_tiles, col_tiles, r, ct);
+      rt_all = (int)r;
+    }
+    Place q;
+    q.g = uniform(in_full ? find_group_wave(s_pref, E, rt_all, lane) : find_group_wave(s_half, E, rt_all, lane));
+    const int s = uniform(group_start<MODE>(s_end, q.g)), e = uniform(s_end[q.g]);
+    q.rt = in_full ? rt_all - uniform(s_pref[q.g]) : (e - s - 1) / BM;
+    q.row0 = s + q.rt * BM;
+    q.rows = e - q.row0 < BM ? e - q.row0 : BM;
+    q.ct = uniform(ct);
+    return q;
+  };
+  auto place_tile = [&](const Place& q, Tile& T) __attribute__((always_inline)) {
+    const int64_t kbytes = p.k / 2, tile_bytes = (p.k + 127) / 128 * 1024;
+    const int col0 = q.ct * BN;
+    const int64_t arow = is_masked(MODE) ? (int64_t)q.g * p.m + q.row0 : (int64_t)q.row0;
+    T.A.origin = pa + arow * kbytes;
+    T.A.ld_bytes = (uint32_t)kbytes;
+    T.A.rows = q.rows;
+    T.A.red = (int)kbytes;
+    T.A.row_tail = T.A.split = 0;
+    T.B.origin = pb + ((int64_t)q.g * p.n + col0) * kbytes;
+    T.B.ld_bytes = (uint32_t)kbytes;
+    T.B.rows = (int)(p.n - col0 < BN ? p.n - col0 : BN);
+    T.B.red = (int)kbytes;
+    T.B.row_tail = T.B.split = 0;
+    T.ldc_bytes = (uint32_t)(esz * p.n);
+    T.cbase = pc + esz * (arow * p.n + col0);
+    T.rows = q.rows;
+    T.cols = T.B.rows;
+    const int64_t xtile = is_masked(MODE) ? (int64_t)q.g * ((p.m + BM - 1) / BM) + q.rt
+                                          : (int64_t)uniform(s_pref[q.g]) + uniform((int)s_half[q.g]) + q.rt;
+    T.sa = p.sa + xtile * tile_bytes;
+    T.sb = p.sb + ((int64_t)q.g * col_tiles + q.ct) * tile_bytes;
+    T.sa_left = 0;
+    T.bias = nullptr;
+    T.bscale = nullptr;
+  };
 
   // Decode tile t (linear index over the output tile grid) into its
   // operand descriptions and output window.
@@ -2041,32 +2275,28 @@ __global__ __launch_bounds__(NT, 1) void grouped_gemm_kernel(Params p) {
       T.cbase = pc + esz * ((int64_t)g * p.k * p.n + (int64_t)row0 * p.n + col0);
       T.rows = A.rows;
       T.cols = B.rows;
-    } else {
+    } else if constexpr (!is_fp4(MODE)) {
       // full phase: row tile rt_all - s_pref[g] of group g; half phase:
       // the last row tile of group g
       const bool in_full = u < full_tiles;
-      int found;
-      if constexpr (is_fp4(MODE)) found = in_full ? find_group(s_pref, E, (int)rt_all) : find_group(s_half, E, (int)rt_all);
-      else found = find_group(in_full ? s_pref : s_half, E, (int)rt_all);
-      const int g = uniform(found);
+      const int g = uniform(find_group(in_full ? s_pref : s_half, E, (int)rt_all));
       const int s = uniform(group_start<MODE>(s_end, g)), e = uniform(s_end[g]);
       const int rt = in_full ? (int)rt_all - uniform(s_pref[g]) : (e - s - 1) / BM;
       const int row0 = s + rt * BM;             // first expert row of the tile
       const int rows = (e - row0) < BM ? (e - row0) : BM;
       const int64_t arow = is_masked(MODE) ? (int64_t)g * p.m + row0 : (int64_t)row0;
-      if constexpr (is_scaled(MODE)) {
+      if constexpr (is_fp8(MODE)) {
         // A(row i, red kk) = X[arow + i, kk];  B(row n, red kk) = W[g, col0 + n, kk]
-        // (one byte per value; fp4: per two, and all of it counted in bytes)
-        const int64_t kbytes = is_fp4(MODE) ? p.k / 2 : p.k;
-        A.origin = pa + arow * kbytes;
-        A.ld_bytes = (uint32_t)kbytes;
+        // (one byte per value)
+        A.origin = pa + arow * p.k;
+        A.ld_bytes = (uint32_t)p.k;
         A.rows = rows;
-        A.red = (int)kbytes;
+        A.red = (int)p.k;
         A.row_tail = 0;
-        B.origin = pb + ((int64_t)g * p.n + col0) * kbytes;
-        B.ld_bytes = (uint32_t)kbytes;
+        B.origin = pb + ((int64_t)g * p.n + col0) * p.k;
+        B.ld_bytes = (uint32_t)p.k;
         B.rows = (int)(p.n - col0 < BN ? p.n - col0 : BN);
-        B.red = (int)kbytes;
+        B.red = (int)p.k;
         B.row_tail = 0;
         T.ldc_bytes = (uint32_t)(esz * p.n);
         T.cbase = pc + esz * (arow * p.n + col0);
@@ -2149,8 +2379,15 @@ __global__ __launch_bounds__(NT, 1) void grouped_gemm_kernel(Params p) {
   // assigned on every path (it stays in scalar registers).
   const int64_t last = total - 1;
   Tile cur;
-  decode_tile(blockIdx.x, cur);
-  issue_prologue(cur);
+  [[maybe_unused]] Place next;      // fp4: the tile after cur
+  if constexpr (is_fp4(MODE)) {
+    place_tile(locate(blockIdx.x), cur);
+    issue_prologue(cur);
+    next = locate((int64_t)blockIdx.x + gridDim.x < total ? (int64_t)blockIdx.x + gridDim.x : last);
+  } else {
+    decode_tile(blockIdx.x, cur);
+    issue_prologue(cur);
+  }
   int prev_stores = 0;    // fp32 stores issued after the current tile's prologue loads
   // The scaled form (alpha != 1 or beta != 0) goes through the LDS epilogue
   // for both output types.
@@ -2174,14 +2411,15 @@ __global__ __launch_bounds__(NT, 1) void grouped_gemm_kernel(Params p) {
                         cur.B, tid, wave, faa, fab, acc, x8);
     } else if constexpr (is_scaled(MODE)) {
       const uint32_t sc_bytes = (uint32_t)(scale_kblocks<MODE>(p.k) * 256);
+      constexpr int kEarly = is_fp4(MODE) ? stores_early<TM, OUT_F32>() : 0;
       if (half)
-        mainloop8_pp<2, is_fp4(MODE)>(sa0, sa1, sa2, sa3, sa0 + OP_BYTES, sa1 + OP_BYTES, sa2 + OP_BYTES,
+        mainloop8_pp<2, is_fp4(MODE), kEarly>(sa0, sa1, sa2, sa3, sa0 + OP_BYTES, sa1 + OP_BYTES, sa2 + OP_BYTES,
                                       sa3 + OP_BYTES, s_sc, cur.A.origin, cur.B.origin, cur.sa, cur.sb, sc_bytes,
-                                      cur.A, cur.B, tid, wave, wm, wn, 0, faa_half, fab, acc);
+                                      cur.A, cur.B, tid, wave, wm, wn, 0, faa_half, fab, acc, prev_stores);
       else
-        mainloop8_pp<TM, is_fp4(MODE)>(sa0, sa1, sa2, sa3, sa0 + OP_BYTES, sa1 + OP_BYTES, sa2 + OP_BYTES,
+        mainloop8_pp<TM, is_fp4(MODE), kEarly>(sa0, sa1, sa2, sa3, sa0 + OP_BYTES, sa1 + OP_BYTES, sa2 + OP_BYTES,
                                        sa3 + OP_BYTES, s_sc, cur.A.origin, cur.B.origin, cur.sa, cur.sb, sc_bytes,
-                                       cur.A, cur.B, tid, wave, wm, wn, wm, faa, fab, acc);
+                                       cur.A, cur.B, tid, wave, wm, wn, wm, faa, fab, acc, prev_stores);
     } else if constexpr (PP_PAIR) {
       // the wave's A rows: 128 wm.. (full height, region wm) or 64 wm.. (half, region 0)
       if (half)
@@ -2203,7 +2441,31 @@ __global__ __launch_bounds__(NT, 1) void grouped_gemm_kernel(Params p) {
                                                     cur.B, tid, wave, faa, fab, acc, prev_stores);
     }
     const int64_t tn = t + gridDim.x;
-    if (OUT_F32 && !STAGED_F32 && !scaled && !is_silu(MODE) && !is_scaled(MODE)) {
+    if constexpr (is_fp4(MODE)) {
+      // every wave is done with the stages, and loads past the end have landed
+      // their zeros: slots 0 to 2 take the next tile's first loads, slot 3 the
+      // output
+      stage_barrier();
+      Tile nxt;
+      place_tile(next, nxt);
+      if (tn < total) issue_prologue(nxt);
+      uint8_t* slab = sa3 + wave * (STAGE_BYTES / NWAVE);
+      const bool whole_lines = ((cur.ldc_bytes | (uint32_t)reinterpret_cast<uintptr_t>(cur.cbase)) & 127u) == 0u;
+#define GG_STORE_EARLY(H, LINES) \
+  store_tile_early<H, OUT_F32, LINES>(cur.cbase, cur.ldc_bytes, cur.rows, cur.cols, wm, wn, lane, acc, slab)
+      if (half) {
+        if (whole_lines) GG_STORE_EARLY(2, true); else GG_STORE_EARLY(2, false);
+        prev_stores = stores_early<2, OUT_F32>();
+      } else {
+        if (whole_lines) GG_STORE_EARLY(TM, true); else GG_STORE_EARLY(TM, false);
+        prev_stores = stores_early<TM, OUT_F32>();
+      }
+#undef GG_STORE_EARLY
+      cur = nxt;
+      // found while the first loads arrive
+      const int64_t tn2 = tn + gridDim.x;
+      next = locate(tn2 < total ? tn2 : last);
+    } else if (OUT_F32 && !STAGED_F32 && !scaled && !is_silu(MODE) && !is_scaled(MODE)) {
       // Every wave is done reading this tile's stages: issue the next
       // tile's prologue loads first, then this tile's stores, so the
       // stores drain while those loads are in flight.  (Loads of stages
