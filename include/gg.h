@@ -826,8 +826,8 @@ gg_status gg_fp4_masked_forward(const void* x, const void* x_scales,
  * gg_moe_few_tokens takes bf16 weights, hidden and inter multiples of 8;
  * gg_fp4_moe_few_tokens takes e2m1 codes [.., k / 2] with packed scales
  * (GG_FP4_WEIGHT), hidden and inter multiples of 32; the activations stay bf16.
- * Sums are fp32 in a fixed order; weights[t, s] silu(.) (.) is rounded to bf16
- * once on the way, out once at the end.  An infinity or NaN of an expert's
+ * Sums are fp32 in a fixed order; weights[t, s] silu(.) (.) is kept to 16 bits of
+ * mantissa on the way (two bf16 values), out is rounded once.  An infinity or NaN of an expert's
  * weights reaches its own tokens only.
  * tokens <= GG_FEW_TOKENS_MAX and tokens * topk <= GG_FEW_SLOTS_MAX
  * (GG_ERR_LIMIT otherwise), and 2 * inter * hidden < 2^31.  No expert that no

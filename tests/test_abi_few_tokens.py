@@ -48,7 +48,7 @@ def test_no_tokens_need_nothing(lib, name, defaults):
 def test_workspace(lib):
     for tokens, topk, inter, e in ((0, 1, 8, 1), (1, 8, 768, 128), (64, 16, 2048, 256), (3, 341, 40, 2048)):
         need = gg.moe_few_tokens_workspace_bytes(tokens, topk, inter, e)
-        assert need == 16 + 16 * min(tokens * topk, e) + tokens * topk * inter * 2
+        assert need == 16 + 16 * min(tokens * topk, e) + tokens * topk * inter * 4
     for args in ((-1, 1, 8, 1), (65, 1, 8, 1), (1, 0, 8, 1), (64, 17, 8, 1), (1, 1, 12, 1), (1, 1, 0, 1), (1, 1, 8, 0),
                  (1, 1, 8, 2049)):
         assert lib.gg_moe_few_tokens_workspace_bytes(*args) == -1
