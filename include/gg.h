@@ -830,7 +830,7 @@ gg_status gg_fp4_masked_forward(const void* x, const void* x_scales,
  * mantissa on the way (two bf16 values), out is rounded once.  An infinity or NaN of an expert's
  * weights reaches its own tokens only.
  * tokens <= GG_FEW_TOKENS_MAX and tokens * topk <= GG_FEW_SLOTS_MAX
- * (GG_ERR_LIMIT otherwise), and 2 * inter * hidden < 2^31.  No expert that no
+ * (GG_ERR_LIMIT otherwise), and 2 * inter * hidden < 2^30.  No expert that no
  * token chose is read.  Errors otherwise as the GEMM entry points; safe to capture
  * in a HIP graph.
  * Cited passage: sglang PR #32385, "Cause" (the decoding step's gate/up, SiLU-mul

@@ -943,8 +943,9 @@ static gg_status few_run(bool four, const void* x, const int32_t* experts, const
     return fail(GG_ERR_BAD_DIM, "hidden and 2 * inter must not exceed GG_MAX_KN");
   if (tokens > GG_FEW_TOKENS_MAX || tokens * (int64_t)topk > GG_FEW_SLOTS_MAX)
     return fail(GG_ERR_LIMIT, "need tokens <= GG_FEW_TOKENS_MAX and tokens * topk <= GG_FEW_SLOTS_MAX");
-  if (2 * inter * hidden >= (int64_t(1) << 31))
-    return fail(GG_ERR_BAD_DIM, "2 * inter * hidden must be below 2^31");
+  // (an expert's rows are one 32-bit buffer range, and offsets past it start at 2^31)
+  if (2 * inter * hidden >= (int64_t(1) << 30))
+    return fail(GG_ERR_BAD_DIM, "2 * inter * hidden must be below 2^30 (2 GiB of bf16)");
   if (!aligned16(x) || !aligned16(w13) || !aligned16(w2) || !aligned16(s13) || !aligned16(s2) || !aligned16(out) ||
       !aligned16(workspace) || !aligned4(experts) || !aligned4(weights))
     return fail(GG_ERR_ALIGNMENT, "pointers must be 16-byte aligned, int32 and fp32 arrays 4-byte aligned");

@@ -14,18 +14,24 @@
 // instruction's operand as they lie in memory, the rows are its 16 columns.
 // 4-bit weights become bf16 in registers (exactly).
 //
-//   up kernel    a workgroup takes an expert and 16 columns of I: rows c of W1
-//                and W3 against x of the tokens that chose the expert; writes
+//   up kernel    a workgroup takes an expert and strips of 8 columns of I: an
+//                instruction's 16 rows are the 8 of W1 and the 8 of W3.  Writes
 //                weight * a to the workspace, as the sum of two bf16 values (a
-//                single one would double the layer's error)
-//   down kernel  a workgroup takes 16 rows of every reached expert's W2 and
-//                adds all experts' shares itself, so out is written once, with
-//                no partial sums in memory
+//                single one would add half as much again to the layer's error)
+//   down kernel  a workgroup takes 8 rows of every reached expert's W2 and adds
+//                all experts' shares itself, so out is written once, with no
+//                partial sums in memory.  Places 8..15 of an instruction are the
+//                same 8 rows at the next values of the reduction, and so are
+//                its columns 8..15: two of its four quarters count
 //
-// Which experts are reached, and by whom, the up kernel's workgroups find for
-// themselves from the expert ids: each wave alone where there are at most 64
-// slots (no barrier, one load ahead of the weights), else in LDS.  The first
-// workgroup of each expert leaves it in the workspace for the down kernel.
+// A compute unit takes in 25 GB/s of weights from memory, whatever it has in
+// flight, so what counts is that all 256 have the same share: hence strips of
+// 8 rows (of 16, one token's 8 experts, 2048 x 768: up 15.0 us for
+// UP_TOKEN, down 12.0 for DOWN_TOKEN; 23 tokens: down 99 for DOWN_BATCH).
+//
+// Which experts are reached, and by whom, a workgroup's first wave finds from
+// the expert ids; the first workgroup of each expert leaves it in the workspace
+// for the down kernel.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -42,10 +48,11 @@ using rows::u32x4r;
 constexpr int kMaxTokens = kFewTokensMax;
 constexpr int kMaxSlots = kFewSlotsMax;
 constexpr int kWaveSlots = 64;                // slots that a wave holds, one a lane
-constexpr int kStrip = 16;                    // weight rows of a workgroup (and columns of a matrix instruction)
+constexpr int kStrip = 8;                     // weight rows of a strip
 constexpr int kUpWaves = 8, kDownWaves = 16;
-constexpr int kPitch = kStrip + 1;            // floats between a token's strips in LDS
-constexpr int kPair = 8;                      // tokens of a down product: two columns each
+constexpr int kPitch = 2 * kStrip + 1;        // floats between a token's sums in LDS
+constexpr int kUpGroups = 4096;               // up workgroups from which on each takes several strips
+constexpr int kQuad = 4;                      // tokens of a down product: four columns each
 constexpr uint32_t kOutside = 0x80000000u;    // an offset past every range here
 
 typedef __bf16 bf16x8f __attribute__((ext_vector_type(8)));
@@ -68,9 +75,8 @@ struct Weights {
 
 __device__ __forceinline__ int wave_index() { return __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)); }
 
-// One reduction step of a wave: 64 bf16 or 128 4-bit values of each of the 16
-// rows, as operands of its matrix instructions.  Lane l holds row l mod 16;
-// operand j covers, of l / 16 = q,
+// One reduction step of an instruction's row: 64 bf16 or 128 4-bit values, as
+// operands of matrix instructions.  Operand j of lane l covers, of q = l / 16,
 //   bf16  values 32 j + 8 q .. + 7      (two operands)
 //   4 bit values 32 q + 8 j .. + 7      (four)
 template <bool FOUR>
@@ -93,27 +99,25 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t range(const void* base, int64_
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, (int)(uint32_t)bytes, 0x00020000);
 }
 
-// Rows row0 .. of an expert's matrix, as far as a strip reaches, as ranges that
-// end with them (rows past the last read as zero).  All scalar.
+// Rows row0 .. row0 + rows - 1 of an expert's matrix and the tiles of scales
+// that hold them, as ranges that end with them (what lies past reads as zero).
+// All scalar.
 template <bool FOUR>
 struct Strip {
   __amdgpu_buffer_rsrc_t w, scales;
   __device__ __forceinline__ Strip(const Weights& m, int64_t expert, int64_t row0, int64_t rows) {
-    constexpr int kSpan = FOUR ? 128 : kStrip;
-    const int64_t span = rows < kSpan ? rows : kSpan;
     const int64_t pitch = FOUR ? m.k / 2 : m.k * 2;
-    w = range(m.w + (expert * m.rows + row0) * pitch, span * pitch);
-    // (the span may begin anywhere in a tile of scales, and reach into the next)
+    w = range(m.w + (expert * m.rows + row0) * pitch, rows * pitch);
     if constexpr (FOUR) {
       const int64_t tile = stages4(m.k) * kStageBytes, tiles = (m.rows + kTileRows - 1) / kTileRows;
       const int64_t first = row0 / kTileRows;
-      scales = range(m.scales + (expert * tiles + first) * tile, (tiles - first < 2 ? tiles - first : 2) * tile);
+      scales = range(m.scales + (expert * tiles + first) * tile, (tiles - first) * tile);
     }
   }
 };
 
-// This lane's place in a strip: the offsets of its row's first values and of
-// their scales.
+// The offsets of this lane's row's first values and of their scales, from a
+// strip's first row on.
 template <bool FOUR>
 struct Lane {
   uint32_t w, scale;
@@ -128,35 +132,43 @@ struct Lane {
   }
 };
 
-// Values that a lane's operand j of a step covers and that a row of k has.
-template <bool FOUR>
-__device__ __forceinline__ bool inside(int step, int q, int j, int k) {
-  return step * Step<FOUR>::kValues + Step<FOUR>::at(q, FOUR ? 0 : j) < k;
-}
-
-template <bool FOUR>
-__device__ __forceinline__ void load_weights(const Strip<FOUR>& s, const Lane<FOUR>& l, int step, int q, int k,
-                                             Raw<FOUR>& r) {
-  if constexpr (FOUR) {
-    const bool in = inside<FOUR>(step, q, 0, k);
-    r.v[0] = load_range(s.w, in ? l.w : kOutside, 64 * step);
-    r.scale = __builtin_amdgcn_raw_buffer_load_b8(s.scales, in ? l.scale : kOutside, kStageBytes * step, 0);
-  } else {
-#pragma unroll
-    for (int j = 0; j < 2; ++j) r.v[j] = load_range(s.w, inside<FOUR>(step, q, j, k) ? l.w + 64 * j : kOutside, 128 * step);
+// HALVES 2: lanes of columns 8..15 take the step after the given one (a step
+// then is two).
+template <bool FOUR, int HALVES>
+struct Reader {
+  static constexpr int kOperands = Step<FOUR>::kOperands;
+  static constexpr int kValues = HALVES * Step<FOUR>::kValues;
+  int k, first;            // values of a row; this lane's first one of step 0
+  __device__ __forceinline__ Reader(int64_t row_values, int col, int q)
+      : k((int)row_values), first((HALVES == 2 && col >= 8 ? Step<FOUR>::kValues : 0) + Step<FOUR>::at(q, 0)) {}
+  __device__ __forceinline__ int steps() const { return (k + kValues - 1) / kValues; }
+  __device__ __forceinline__ bool inside(int step, int j) const {
+    return step * kValues + first + (FOUR ? 0 : Step<FOUR>::at(0, j)) < k;
   }
-}
-
-// The rows' operands: bf16 rows from `at` on (this lane's first value's offset,
-// or kOutside).
-template <bool FOUR>
-__device__ __forceinline__ void load_rows(const __amdgpu_buffer_rsrc_t& rs, uint32_t at, int base, int step, int q, int k,
-                                          u32x4r (&v)[Step<FOUR>::kOperands]) {
+  __device__ __forceinline__ void weights(const Strip<FOUR>& s, const Lane<FOUR>& l, bool second, int step,
+                                          Raw<FOUR>& r) const {
+    const uint32_t half = HALVES == 2 && second ? 1u : 0u;
+    if constexpr (FOUR) {
+      const bool in = inside(step, 0);
+      r.v[0] = load_range(s.w, in ? l.w + 64u * half : kOutside, kValues / 2 * step);
+      r.scale = __builtin_amdgcn_raw_buffer_load_b8(s.scales, in ? l.scale + kStageBytes * half : kOutside,
+                                                    HALVES * kStageBytes * step, 0);
+    } else {
 #pragma unroll
-  for (int j = 0; j < Step<FOUR>::kOperands; ++j)
-    v[j] = load_range(rs, inside<FOUR>(step, q, j, k) ? at + (uint32_t)(2 * (Step<FOUR>::at(0, j))) : kOutside,
-                      base + 2 * Step<FOUR>::kValues * step);
-}
+      for (int j = 0; j < 2; ++j)
+        r.v[j] = load_range(s.w, inside(step, j) ? l.w + 128u * half + 64u * j : kOutside, 2 * kValues * step);
+    }
+  }
+  // The rows' operands: bf16 rows; `at` is the offset of this lane's row's
+  // first value of step 0 (first, that is), or kOutside.
+  __device__ __forceinline__ void rows(const __amdgpu_buffer_rsrc_t& rs, uint32_t at, int base, int step,
+                                       u32x4r (&v)[kOperands]) const {
+#pragma unroll
+    for (int j = 0; j < kOperands; ++j)
+      v[j] = load_range(rs, inside(step, j) ? at + 2u * (uint32_t)Step<FOUR>::at(0, j) : kOutside,
+                        base + 2 * kValues * step);
+  }
+};
 
 template <bool FOUR>
 __device__ __forceinline__ bf16x8f operand(const Raw<FOUR>& r, int j) {
@@ -173,21 +185,26 @@ __device__ __forceinline__ bf16x8f operand(const Raw<FOUR>& r, int j) {
   }
 }
 
-// First row of a strip's span, and the row in it of the strip's place i (0..15).
-// 4 bits: four runs of 4 rows 32 apart, whose scales are 64 consecutive bytes
-// of every stage.
+// Strips' first rows, and the row of a strip's place i (0..7) from there.  4
+// bits: strips share spans of 128 rows, each two runs of 4 rows 32 apart, whose
+// scales are 32 consecutive bytes of every stage.
+template <bool FOUR>
+__host__ __device__ inline int64_t strips(int64_t rows) {
+  return FOUR ? (rows + 127) / 128 * 16 : (rows + kStrip - 1) / kStrip;
+}
 template <bool FOUR>
 __device__ __forceinline__ int64_t strip_first(int strip) {
-  return FOUR ? strip / 8 * 128 : (int64_t)strip * kStrip;
+  return FOUR ? strip / 16 * 128 : (int64_t)strip * kStrip;
 }
 template <bool FOUR>
 __device__ __forceinline__ int strip_place(int strip, int i) {
-  return FOUR ? 32 * (i & 3) + 4 * (strip % 8) + (i >> 2) : i;
+  return FOUR ? 32 * (i & 3) + 2 * (strip % 16) + (i >> 2) : i;
 }
 
-template <bool FOUR>
-__host__ __device__ inline int64_t strips(int64_t rows) {
-  return FOUR ? (rows + 127) / 128 * 8 : (rows + kStrip - 1) / kStrip;
+// Workgroup b of n runs on XCD b mod 8: neighbouring strips, which share cache
+// lines of scales, to one XCD, 4 in a row.
+__device__ __forceinline__ int strip_of(int b, int n) {
+  return n % 32 != 0 ? b : b / 32 * 32 + b % 8 * 4 + b / 8 % 4;
 }
 
 struct Few {
@@ -201,6 +218,7 @@ struct Few {
   uint16_t* act;            //   and rows of weight * a [slots, 2, inter]: its bf16 value, and what that left
   void* out;                // [tokens, hidden]
   bool out_f32;
+  int32_t strips_each;      // strips of an up workgroup
 };
 
 __device__ __forceinline__ uint64_t lanes_before(int lane) { return (1ull << lane) - 1ull; }
@@ -211,47 +229,65 @@ __device__ __forceinline__ uint64_t lane_value64(uint64_t v, int lane) {
   return (uint64_t)hi << 32 | lo;
 }
 
-// The reduction of one expert's gate and up strip over this wave's steps, for
-// up to 16 BLOCKS tokens.
+// use(a, i) on items i = 0 .. n - 1 with issue(a, i) kAhead of them ahead, a
+// their place.  Whole rounds in the loop, the rest after it: an issue that may
+// be skipped in the loop would make the compiler wait for all loads on every
+// path, and a load out of range costs as much of the address unit's time as
+// any other.
+template <int kAhead, typename Issue, typename Use>
+__device__ __forceinline__ void pipelined(int n, const Issue& issue, const Use& use) {
+#pragma unroll
+  for (int a = 0; a < kAhead; ++a)
+    if (a < n) issue(a, a);
+  int i = 0;
+  for (; i + 2 * kAhead <= n; i += kAhead) {
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a) {
+      use(a, i + a);
+      issue(a, i + kAhead + a);
+    }
+  }
+#pragma unroll
+  for (int a = 0; a < kAhead; ++a) {
+    if (i + a < n) use(a, i + a);
+    if (i + kAhead + a < n) issue(a, i + kAhead + a);
+  }
+#pragma unroll
+  for (int a = 0; a < kAhead; ++a)
+    if (i + kAhead + a < n) use(a, i + kAhead + a);
+}
+
+// The reduction of one strip over this wave's steps, for up to 16 BLOCKS
+// tokens.
 template <bool FOUR, int BLOCKS>
-__device__ __forceinline__ void up_steps(const Few& p, const Strip<FOUR>& gate, const Strip<FOUR>& up, const Lane<FOUR>& lg,
-                                         const Lane<FOUR>& lu, const int32_t* tokens, int found, int wave, int col, int q,
-                                         f32x4f (&ag)[4], f32x4f (&au)[4]) {
-  using S = Step<FOUR>;
-  constexpr int kAhead = BLOCKS == 1 ? (FOUR ? 3 : 4) : BLOCKS == 2 ? 2 : 1;
-  const int k = p.hidden, steps = (k + S::kValues - 1) / S::kValues;
-  const __amdgpu_buffer_rsrc_t xs = range(p.x, (int64_t)p.tokens * k * 2);
+__device__ __forceinline__ void up_steps(const Few& p, const Strip<FOUR>& s, const Lane<FOUR>& l, const int32_t* tokens,
+                                         int found, int wave, int col, int q, f32x4f (&acc)[4]) {
+  constexpr int kAhead = BLOCKS == 1 ? 4 : BLOCKS == 2 ? 2 : 1;
+  const Reader<FOUR, 1> rd(p.hidden, col, q);
+  const int steps = rd.steps();
+  const __amdgpu_buffer_rsrc_t xs = range(p.x, (int64_t)p.tokens * p.hidden * 2);
   uint32_t xat[BLOCKS];
 #pragma unroll
   for (int b = 0; b < BLOCKS; ++b)
-    xat[b] = 16 * b + col < found ? (uint32_t)(tokens[16 * b + col] * k + S::at(q, 0)) * 2u : kOutside;
-  Raw<FOUR> g[kAhead], u[kAhead];
-  u32x4r x[kAhead][BLOCKS][S::kOperands];
-  auto issue = [&](int a, int step) __attribute__((always_inline)) {
+    xat[b] = 16 * b + col < found ? (uint32_t)(tokens[16 * b + col] * p.hidden + rd.first) * 2u : kOutside;
+  Raw<FOUR> w[kAhead];
+  u32x4r x[kAhead][BLOCKS][Step<FOUR>::kOperands];
+  auto issue = [&](int a, int i) __attribute__((always_inline)) {
+    const int step = wave + kUpWaves * i;
 #pragma unroll
-    for (int b = 0; b < BLOCKS; ++b) load_rows<FOUR>(xs, xat[b], 0, step, q, k, x[a][b]);
-    load_weights<FOUR>(gate, lg, step, q, k, g[a]);
-    load_weights<FOUR>(up, lu, step, q, k, u[a]);
+    for (int b = 0; b < BLOCKS; ++b) rd.rows(xs, xat[b], 0, step, x[a][b]);
+    rd.weights(s, l, false, step, w[a]);
   };
+  auto use = [&](int a, int) __attribute__((always_inline)) {
 #pragma unroll
-  for (int a = 0; a < kAhead; ++a) issue(a, wave + kUpWaves * a);
-  for (int s0 = wave; s0 < steps; s0 += kUpWaves * kAhead) {
+    for (int j = 0; j < Step<FOUR>::kOperands; ++j) {
+      const bf16x8f wo = operand<FOUR>(w[a], j);
 #pragma unroll
-    for (int a = 0; a < kAhead; ++a) {
-      // (steps past the last are zeros)
-#pragma unroll
-      for (int j = 0; j < S::kOperands; ++j) {
-        const bf16x8f wg = operand<FOUR>(g[a], j), wu = operand<FOUR>(u[a], j);
-#pragma unroll
-        for (int b = 0; b < BLOCKS; ++b) {
-          const bf16x8f xo = __builtin_bit_cast(bf16x8f, x[a][b][j]);
-          ag[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wg, xo, ag[b], 0, 0, 0);
-          au[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wu, xo, au[b], 0, 0, 0);
-        }
-      }
-      issue(a, s0 + kUpWaves * (kAhead + a));
+      for (int b = 0; b < BLOCKS; ++b)
+        acc[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wo, __builtin_bit_cast(bf16x8f, x[a][b][j]), acc[b], 0, 0, 0);
     }
-  }
+  };
+  pipelined<kAhead>((steps - wave + kUpWaves - 1) / kUpWaves, issue, use);
 }
 
 // SMALL: at most 64 slots.
@@ -259,63 +295,63 @@ template <bool FOUR, bool SMALL>
 __global__ __launch_bounds__(64 * kUpWaves, 4) void few_up_kernel(Few p) {
   __shared__ int32_t s_expert[SMALL ? 1 : kMaxSlots];
   __shared__ uint32_t s_bits[SMALL ? 1 : GG_MAX_GROUPS_DEV / 32];
-  __shared__ int32_t s_token[SMALL ? kUpWaves : 1][kMaxTokens];
-  __shared__ float s_share[SMALL ? kUpWaves : 1][kMaxTokens];
-  __shared__ int32_t s_info[2];             // the expert's tokens, and its workspace row
-  __shared__ float s_sum[kUpWaves][2][kStrip][kPitch];
+  __shared__ int32_t s_token[kMaxTokens];   // the expert's tokens,
+  __shared__ int32_t s_slot[kMaxTokens];    //   the slots that name it,
+  __shared__ int32_t s_more[kMaxTokens];    //   and how many more of the token's do
+  __shared__ float s_share[kMaxTokens];
+  __shared__ int32_t s_info[3];             // their number, the first one's workspace row, the expert
+  __shared__ float s_sum[kUpWaves][16][kPitch];
   const int tid = threadIdx.x, lane = tid & 63, wave = wave_index();
-  const int own = SMALL ? wave : 0;         // SMALL: every wave has its copy of the lists
   const int slots = p.tokens * p.topk;
-  const int strip = blockIdx.x, d = blockIdx.y;
-  int expert, found, base;
+  const int d = blockIdx.y;
+  const bool leader = blockIdx.x == 0;      // of the expert's workgroups
 
+  // Wave 0 finds the d-th reached expert and its tokens (one that names it
+  // twice counts once, with both shares).  An expert has as many workspace rows
+  // as it has slots.
   if constexpr (SMALL) {
-    int e = lane < slots ? p.experts[lane] : -1;
-    const float w = p.share && lane < slots ? p.share[lane] : 1.0f;
-    e = e < p.num_groups ? e : -1;
-    // experts in the order of their first slots; each leaves as many workspace
-    // rows as it has slots
-    uint64_t left = __ballot(e >= 0), mine = 0;
-    int n = 0;
-    base = 0;
-    expert = 0;
-    while (left != 0ull) {
-      const int at = __builtin_amdgcn_readlane(e, __ffsll((unsigned long long)left) - 1);
-      const uint64_t same = __ballot(e == at);
-      left &= ~same;
-      if (n == d) {
-        mine = same;
-        expert = at;
-        if (strip != 0 || d != 0) break;        // (the first workgroup counts them all)
-      } else if (n < d) {
-        base += __popcll(same);
-      }
-      ++n;
-    }
-    if (strip == 0 && d == 0 && tid == 0) *p.count = n;
-    if (mine == 0ull) return;
-    // its tokens, by slot: a token that names it twice counts once, with both
-    // shares
-    uint64_t who = 0;
-    found = 0;
-    int last = -1;
-    float sum = 0.f;
-    for (uint64_t m = mine; m != 0ull; m &= m - 1ull) {
-      const int s = __ffsll((unsigned long long)m) - 1, t = s / p.topk;
-      const float v = rows::lane_value(w, s);
-      if (t != last) {
-        if (lane == found) {
-          s_token[own][found] = t;
+    if (wave == 0) {
+      int e = lane < slots ? p.experts[lane] : -1;
+      e = e < p.num_groups ? e : -1;
+      // experts in the order of their first slots
+      uint64_t left = __ballot(e >= 0), mine = 0;
+      int n = 0, base = 0, expert = 0;
+      while (left != 0ull) {
+        const int at = __builtin_amdgcn_readlane(e, __ffsll((unsigned long long)left) - 1);
+        const uint64_t same = __ballot(e == at);
+        left &= ~same;
+        if (n == d) {
+          mine = same;
+          expert = at;
+          if (!leader || d != 0) break;         // (the first workgroup counts them all)
+        } else if (n < d) {
+          base += __popcll(same);
         }
-        ++found;
-        sum = 0.f;
-        last = t;
-        who |= 1ull << t;
+        ++n;
       }
-      sum += v;
-      if (lane == 0) s_share[own][found - 1] = sum;
+      const int t = lane / p.topk, start = t * p.topk, end = start + p.topk;
+      const uint64_t token = mine & ~lanes_before(start < 64 ? start : 63) & (end < 64 ? lanes_before(end) : ~0ull);
+      const bool first = ((mine >> lane) & 1ull) && (token & lanes_before(lane)) == 0ull;
+      const uint64_t firsts = __ballot(first);
+      if (first) {
+        const int i = __popcll(firsts & lanes_before(lane));
+        s_token[i] = t;
+        s_slot[i] = lane;
+        s_more[i] = __popcll(token) - 1;
+      }
+      if (lane == 0) {
+        s_info[0] = __popcll(firsts);
+        s_info[1] = base;
+        s_info[2] = expert;
+      }
+      if (leader) {
+        uint64_t who = 0;
+        for (uint64_t m = firsts; m != 0ull; m &= m - 1ull)
+          who |= 1ull << __builtin_amdgcn_readlane(t, __ffsll((unsigned long long)m) - 1);
+        if (lane == 0 && mine != 0ull) p.reached[d] = Reached{expert, base, who};
+        if (lane == 0 && d == 0) *p.count = n;
+      }
     }
-    if (strip == 0 && tid == 0) p.reached[d] = Reached{expert, base, who};
   } else {
     for (int i = tid; i < GG_MAX_GROUPS_DEV / 32; i += 64 * kUpWaves) s_bits[i] = 0u;
     __syncthreads();
@@ -325,105 +361,129 @@ __global__ __launch_bounds__(64 * kUpWaves, 4) void few_up_kernel(Few p) {
       if (e >= 0 && e < p.num_groups) atomicOr(&s_bits[e >> 5], 1u << (e & 31));
     }
     __syncthreads();
-    // the d-th reached expert, by index
-    const uint32_t word = s_bits[lane];
-    int upto = __popc(word);
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const int v = __shfl_up(upto, (unsigned)o, 64);
-      if (lane >= o) upto += v;
-    }
-    const int reached = __shfl(upto, 63, 64);
-    if (strip == 0 && d == 0 && tid == 0) *p.count = reached;
-    if (d >= reached) return;
-    const int at = __ffsll((unsigned long long)__ballot(upto > d)) - 1;
-    const uint32_t bits = (uint32_t)__shfl((int)word, at, 64);
-    const int nth = d - (__shfl(upto, at, 64) - __popc(bits));
-    const int bit = lane & 31;
-    const uint64_t hit = __ballot(((bits >> bit) & 1u) && __popc(bits & ((1u << bit) - 1u)) == nth);
-    expert = __builtin_amdgcn_readfirstlane(32 * at + __ffsll((unsigned long long)hit) - 1);
     if (wave == 0) {
-      int count = 0, before = 0;
-      uint64_t who = 0;
-      for (int s0 = 0; s0 < slots; s0 += 64) {
-        const int s = s0 + lane;
-        const int e = s < slots ? s_expert[s] : -1;
-        const int t = s < slots ? s / p.topk : 0;
-        bool mine = e == expert;
-        float w = 0.f;
-        if (mine) {
-          for (int j = t * p.topk; j < (t + 1) * p.topk; ++j) {
-            if (s_expert[j] != expert) continue;
-            if (j < s) mine = false;
-            w += p.share ? p.share[j] : 1.0f;
-          }
-        }
-        const uint64_t m = __ballot(mine);
-        before += __popcll(__ballot(e >= 0 && e < expert));
-        if (mine) {
-          const int i = count + __popcll(m & lanes_before(lane));
-          s_token[0][i] = t;
-          s_share[0][i] = w;
-          who |= 1ull << t;
-        }
-        count += __popcll(m);
-      }
+      // experts by index
+      const uint32_t word = s_bits[lane];
+      int upto = __popc(word);
 #pragma unroll
-      for (int o = 32; o > 0; o >>= 1) who |= __shfl_xor((unsigned long long)who, o, 64);
-      if (lane == 0) {
-        s_info[0] = count;
-        s_info[1] = before;
-        if (strip == 0) p.reached[d] = Reached{expert, before, who};
+      for (int o = 1; o < 64; o <<= 1) {
+        const int v = __shfl_up(upto, (unsigned)o, 64);
+        if (lane >= o) upto += v;
       }
+      const int reached = __shfl(upto, 63, 64);
+      if (leader && d == 0 && lane == 0) *p.count = reached;
+      int found = 0;
+      if (d < reached) {
+        const int at = __ffsll((unsigned long long)__ballot(upto > d)) - 1;
+        const uint32_t bits = (uint32_t)__shfl((int)word, at, 64);
+        const int nth = d - (__shfl(upto, at, 64) - __popc(bits));
+        const int bit = lane & 31;
+        const uint64_t hit = __ballot(((bits >> bit) & 1u) && __popc(bits & ((1u << bit) - 1u)) == nth);
+        const int expert = __builtin_amdgcn_readfirstlane(32 * at + __ffsll((unsigned long long)hit) - 1);
+        int base = 0;
+        uint64_t who = 0;
+        for (int s0 = 0; s0 < slots; s0 += 64) {
+          const int s = s0 + lane;
+          const int e = s < slots ? s_expert[s] : -1;
+          base += __popcll(__ballot(e >= 0 && e < expert));
+          if (__ballot(e == expert) == 0ull) continue;
+          const int t = s / p.topk;
+          bool first = e == expert;
+          int more = 0;
+          if (first) {
+            for (int j = t * p.topk; j < s; ++j) first = first && s_expert[j] != expert;
+            for (int j = s + 1; j < (t + 1) * p.topk; ++j) more += s_expert[j] == expert ? 1 : 0;
+          }
+          const uint64_t firsts = __ballot(first);
+          if (first) {
+            const int i = found + __popcll(firsts & lanes_before(lane));
+            s_token[i] = t;
+            s_slot[i] = s;
+            s_more[i] = more;
+          }
+          found += __popcll(firsts);
+          for (uint64_t m = firsts; m != 0ull; m &= m - 1ull)
+            who |= 1ull << __builtin_amdgcn_readlane(t, __ffsll((unsigned long long)m) - 1);
+        }
+        if (lane == 0) {
+          s_info[1] = base;
+          s_info[2] = expert;
+          if (leader) p.reached[d] = Reached{expert, base, who};
+        }
+      }
+      if (lane == 0) s_info[0] = found;
     }
-    __syncthreads();
-    found = __builtin_amdgcn_readfirstlane(s_info[0]);
-    base = s_info[1];
   }
+  __syncthreads();
+  const int found = __builtin_amdgcn_readfirstlane(s_info[0]);
+  if (found == 0) return;
+  const int base = __builtin_amdgcn_readfirstlane(s_info[1]);
+  const int expert = __builtin_amdgcn_readfirstlane(s_info[2]);
+  // its tokens' shares: on their way while the weights are read
+  float share = 1.0f;
+  if (tid < found && p.share) share = p.share[s_slot[tid]];
 
   const int col = lane & 15, q = lane >> 4;
-  const int64_t row0 = strip_first<FOUR>(strip);
-  const int place = strip_place<FOUR>(strip, col);
-  const Strip<FOUR> gate(p.up, expert, row0, p.inter - row0), up(p.up, expert, p.inter + row0, p.inter - row0);
-  const Lane<FOUR> lg(p.up, row0, place, q), lu(p.up, p.inter + row0, place, q);
-  f32x4f ag[4], au[4];
+  const int n = (int)strips<FOUR>(p.inter);
+  const int block = p.strips_each == 1 ? strip_of(blockIdx.x, gridDim.x) : (int)blockIdx.x;
+  for (int z = 0; z < p.strips_each; ++z) {
+    const int strip = block * p.strips_each + z;
+    if (strip >= n) break;
+    const int64_t row0 = strip_first<FOUR>(strip);
+    // places 0..7 rows of W1, 8..15 the same rows of W3
+    const Strip<FOUR> s(p.up, expert, row0, 2 * (int64_t)p.inter - row0);
+    const Lane<FOUR> l(p.up, row0, strip_place<FOUR>(strip, col & 7) + (col >= 8 ? p.inter : 0), q);
+    f32x4f acc[4];
 #pragma unroll
-  for (int b = 0; b < 4; ++b) ag[b] = au[b] = f32x4f{0.f, 0.f, 0.f, 0.f};
-  if (found <= 16) up_steps<FOUR, 1>(p, gate, up, lg, lu, s_token[own], found, wave, col, q, ag, au);
-  else if (found <= 32) up_steps<FOUR, 2>(p, gate, up, lg, lu, s_token[own], found, wave, col, q, ag, au);
-  else up_steps<FOUR, 4>(p, gate, up, lg, lu, s_token[own], found, wave, col, q, ag, au);
-  // the waves' shares of the reduction, added in order; lane l holds token l
-  // mod 16, places 4 (l / 16) .. + 3
-#pragma unroll
-  for (int b = 0; b < 4; ++b) {
-    if (16 * b >= found) break;
-    if (b > 0) __syncthreads();
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      s_sum[wave][0][col][4 * q + r] = ag[b][r];
-      s_sum[wave][1][col][4 * q + r] = au[b][r];
+    for (int b = 0; b < 4; ++b) acc[b] = f32x4f{0.f, 0.f, 0.f, 0.f};
+    if (found <= 16) up_steps<FOUR, 1>(p, s, l, s_token, found, wave, col, q, acc);
+    else if (found <= 32) up_steps<FOUR, 2>(p, s, l, s_token, found, wave, col, q, acc);
+    else up_steps<FOUR, 4>(p, s, l, s_token, found, wave, col, q, acc);
+    if (z == 0 && tid < found) {
+      if (s_more[tid] && p.share) {              // the token's other slots that name the expert
+        for (int j = s_slot[tid] + 1; j < (s_token[tid] + 1) * p.topk; ++j)
+          if (p.experts[j] == expert) share += p.share[j];
+      } else {
+        share += (float)s_more[tid];
+      }
+      s_share[tid] = share;
     }
-    __syncthreads();
-    if (tid < kStrip * kStrip) {
-      const int t = 16 * b + (tid >> 4), i = tid & 15;
-      const int64_t c = row0 + strip_place<FOUR>(strip, i);
-      if (t < found && c < p.inter) {
-        float g = 0.f, u = 0.f;
+    // the waves' parts of the reduction, added in order; lane l holds token l
+    // mod 16, places 4 (l / 16) .. + 3
 #pragma unroll
-        for (int w = 0; w < kUpWaves; ++w) {
-          g += s_sum[w][0][tid >> 4][i];
-          u += s_sum[w][1][tid >> 4][i];
+    for (int b = 0; b < 4; ++b) {
+      if (16 * b >= found) break;
+      if (b > 0 || z > 0) __syncthreads();
+#pragma unroll
+      for (int r = 0; r < 4; ++r) s_sum[wave][col][4 * q + r] = acc[b][r];
+      __syncthreads();
+      if (tid < 16 * kStrip) {
+        const int i = tid & (kStrip - 1), t = 16 * b + tid / kStrip;
+        const int64_t c = row0 + strip_place<FOUR>(strip, i);
+        if (t < found && c < p.inter) {
+          float g = 0.f, u = 0.f;
+#pragma unroll
+          for (int w = 0; w < kUpWaves; ++w) {
+            g += s_sum[w][tid / kStrip][i];
+            u += s_sum[w][tid / kStrip][kStrip + i];
+          }
+          const float a = g * __builtin_amdgcn_rcpf(1.0f + __expf(-g)) * u * s_share[t];
+          __bf16* to = reinterpret_cast<__bf16*>(p.act) + (int64_t)(base + t) * 2 * p.inter + c;
+          const __bf16 high = (__bf16)a;
+          const float left = a - (float)high;
+          to[0] = high;
+          // (an infinity or NaN is its own value, with nothing left)
+          to[p.inter] = (__bf16)(rows::finite(left) ? left : 0.f);
         }
-        const float a = g * __builtin_amdgcn_rcpf(1.0f + __expf(-g)) * u * s_share[own][t];
-        __bf16* to = reinterpret_cast<__bf16*>(p.act) + (int64_t)(base + t) * 2 * p.inter + c;
-        const __bf16 high = (__bf16)a;
-        const float left = a - (float)high;
-        to[0] = high;
-        // (an infinity or NaN is its own value, with nothing left)
-        to[p.inter] = (__bf16)(rows::finite(left) ? left : 0.f);
       }
     }
   }
+}
+
+// The value of the lane opposite in its half of a 16-lane row (7 - i for i).
+__device__ __forceinline__ float half_mirror(float v) {
+  return __builtin_bit_cast(float,
+                            __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0x141, 0xf, 0xf, true));
 }
 
 // TOKENS: at most.
@@ -441,18 +501,18 @@ __global__ __launch_bounds__(64 * kDownWaves) void few_down_kernel(Few p) {
     have = first;
     if (first + lane < most) mine = p.reached[first + lane];
   };
-  const int strip = blockIdx.x;
+  const int strip = strip_of(blockIdx.x, gridDim.x);
   const int col = lane & 15, q = lane >> 4;
-
-  using S = Step<FOUR>;
-  const int k = p.inter, steps = (k + S::kValues - 1) / S::kValues;
+  const bool second = col >= 8;
+  const Reader<FOUR, 2> rd(p.inter, col, q);
+  const int k = p.inter, steps = rd.steps();
   const int64_t row0 = strip_first<FOUR>(strip);
-  const Lane<FOUR> ll(p.down, row0, strip_place<FOUR>(strip, col), q);
+  const Lane<FOUR> l(p.down, row0, strip_place<FOUR>(strip, col & 7), q);
   const __amdgpu_buffer_rsrc_t acts = range(p.act, (int64_t)slots * 4 * k);
-  // columns 0..7 are the bf16 values of 8 of an expert's tokens, 8..15 what
-  // those left
-  const int member = col & (kPair - 1);
-  const uint32_t act_at = (uint32_t)((2 * member + (col >> 3)) * k + S::at(q, 0)) * 2u;
+  // columns 0..3 are the bf16 values of 4 of an expert's tokens, 7..4 what those
+  // left; 8..15 the same at the step's second half
+  const int member = (col & 4) ? 3 - (col & 3) : col & 3;
+  const uint32_t act_at = (uint32_t)((2 * member + ((col >> 2) & 1)) * k + rd.first) * 2u;
   for (int i = lane; i < TOKENS * kStrip / 4; i += 64)
     reinterpret_cast<f32x4f*>(&s_out[wave][0][0])[i] = f32x4f{0.f, 0.f, 0.f, 0.f};
   fetch(0);
@@ -466,85 +526,75 @@ __global__ __launch_bounds__(64 * kDownWaves) void few_down_kernel(Few p) {
     int expert, base, step;
     uint64_t tokens;
   };
-  int at = (int)((int64_t)items * wave / kDownWaves);
-  int d = at / steps, step = at - d * steps;
+  const int begin = (int)((int64_t)items * wave / kDownWaves);
+  int d = begin / steps, step = begin - d * steps;
   auto next = [&]() {
-    Item i = {0, 0, 0, 0ull};                    // (past the wave's last item: no rows)
-    if (at < end) {
-      if (d - have >= 64) fetch(d & ~63);
-      i.expert = __builtin_amdgcn_readlane(mine.expert, d & 63);
-      i.base = __builtin_amdgcn_readlane(mine.base, d & 63);
-      i.tokens = lane_value64(mine.tokens, d & 63);
-      i.step = step;
-      ++at;
-      if (++step == steps) {
-        step = 0;
-        ++d;
-      }
+    if (d - have >= 64) fetch(d & ~63);
+    Item i;
+    i.expert = __builtin_amdgcn_readlane(mine.expert, d & 63);
+    i.base = __builtin_amdgcn_readlane(mine.base, d & 63);
+    i.tokens = lane_value64(mine.tokens, d & 63);
+    i.step = step;
+    if (++step == steps) {
+      step = 0;
+      ++d;
     }
     return i;
   };
-  constexpr int kAhead = FOUR ? 4 : 6;
+  constexpr int kAhead = 4;
   Raw<FOUR> w[kAhead];
-  u32x4r v[kAhead][S::kOperands];
-  Item items_ahead[kAhead];
-  auto issue = [&](int a) __attribute__((always_inline)) {
-    const Item i = items_ahead[a] = next();
+  u32x4r v[kAhead][Step<FOUR>::kOperands];
+  Item ahead[kAhead];
+  auto issue = [&](int a, int) __attribute__((always_inline)) {
+    const Item i = ahead[a] = next();
     const int found = __popcll(i.tokens);
-    load_rows<FOUR>(acts, member < found ? act_at : kOutside, 4 * i.base * k, i.step, q, k, v[a]);
-    const Strip<FOUR> s(p.down, i.expert, row0, i.tokens ? p.hidden - row0 : 0);
-    load_weights<FOUR>(s, ll, i.step, q, k, w[a]);
+    rd.rows(acts, member < found ? act_at : kOutside, 4 * i.base * k, i.step, v[a]);
+    rd.weights(Strip<FOUR>(p.down, i.expert, row0, p.hidden - row0), l, second, i.step, w[a]);
   };
-  auto multiply = [&](const Raw<FOUR>& wr, const u32x4r (&vr)[S::kOperands], f32x4f c) __attribute__((always_inline)) {
+  auto multiply = [&](const Raw<FOUR>& wr, const u32x4r (&vr)[Step<FOUR>::kOperands], f32x4f c)
+      __attribute__((always_inline)) {
 #pragma unroll
-    for (int j = 0; j < S::kOperands; ++j)
+    for (int j = 0; j < Step<FOUR>::kOperands; ++j)
       c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(operand<FOUR>(wr, j), __builtin_bit_cast(bf16x8f, vr[j]), c, 0, 0, 0);
     return c;
   };
-  // Adds tokens 8 b .. of an expert's product to the wave's sums.  (Each
+  // Adds tokens 4 b .. of an expert's product to the wave's sums.  (Each
   // expert's product is one of its own, so that a weight that is not finite
-  // reaches the expert's own tokens only.)
+  // reaches the expert's own tokens only.)  Lanes 0..31 hold the first half's
+  // rows in columns 0..7, lanes 32..63 the second's in 8..15.
   auto add = [&](f32x4f part, uint64_t tokens, int b) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) part[e] += rows::row_ror<kPair>(part[e]);
-    const int i = kPair * b + col;
-    if (col < kPair && i < __popcll(tokens)) {
+    for (int e = 0; e < 4; ++e) part[e] += half_mirror(part[e]);
+    const int i = kQuad * b + (col & 3);
+    if ((col & 4) == 0 && i < __popcll(tokens)) {
       uint64_t left = tokens;
       for (int z = 0; z < i; ++z) left &= left - 1ull;
-      f32x4f* to = reinterpret_cast<f32x4f*>(&s_out[wave][__ffsll((unsigned long long)left) - 1][4 * q]);
-      *to = *to + part;
+      f32x4f* to = reinterpret_cast<f32x4f*>(&s_out[wave][__ffsll((unsigned long long)left) - 1][4 * (q & 1)]);
+      if (q < 2 && !second) *to = *to + part;
+      if (q >= 2 && second) *to = *to + part;
     }
   };
-  if (at < end) {
-    int left = end - at;
-    f32x4f part = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int a = 0; a < kAhead; ++a) issue(a);
-    int expert = items_ahead[0].expert;
-    uint64_t tokens = items_ahead[0].tokens;
-    for (; left > 0; left -= kAhead) {
-#pragma unroll
-      for (int a = 0; a < kAhead; ++a) {
-        const Item i = items_ahead[a];
-        if (i.tokens && i.expert != expert) {
-          add(part, tokens, 0);
-          part = f32x4f{0.f, 0.f, 0.f, 0.f};
-          expert = i.expert;
-          tokens = i.tokens;
-        }
-        part = multiply(w[a], v[a], part);
-        const int found = __popcll(i.tokens);
-        for (int b = 1; kPair * b < found; ++b) {
-          u32x4r more[S::kOperands];
-          load_rows<FOUR>(acts, kPair * b + member < found ? act_at : kOutside, 4 * (i.base + kPair * b) * k, i.step, q, k,
-                          more);
-          add(multiply(w[a], more, f32x4f{0.f, 0.f, 0.f, 0.f}), i.tokens, b);
-        }
-        issue(a);
-      }
+  f32x4f part = {0.f, 0.f, 0.f, 0.f};
+  int expert = -1;
+  uint64_t tokens = 0;
+  auto use = [&](int a, int) __attribute__((always_inline)) {
+    const Item i = ahead[a];
+    if (i.expert != expert) {
+      add(part, tokens, 0);
+      part = f32x4f{0.f, 0.f, 0.f, 0.f};
+      expert = i.expert;
+      tokens = i.tokens;
     }
-    add(part, tokens, 0);
-  }
+    part = multiply(w[a], v[a], part);
+    const int found = __popcll(i.tokens);
+    for (int b = 1; kQuad * b < found; ++b) {
+      u32x4r more[Step<FOUR>::kOperands];
+      rd.rows(acts, kQuad * b + member < found ? act_at : kOutside, 4 * (i.base + kQuad * b) * k, i.step, more);
+      add(multiply(w[a], more, f32x4f{0.f, 0.f, 0.f, 0.f}), i.tokens, b);
+    }
+  };
+  pipelined<kAhead>(end - begin, issue, use);
+  add(part, tokens, 0);
   __syncthreads();
   for (int o = tid; o < p.tokens * kStrip; o += 64 * kDownWaves) {
     const int t = o / kStrip, i = o % kStrip;
@@ -559,11 +609,15 @@ __global__ __launch_bounds__(64 * kDownWaves) void few_down_kernel(Few p) {
 }
 
 template <bool FOUR>
-hipError_t launch_four(const Few& p, hipStream_t stream) {
+hipError_t launch_four(Few p, hipStream_t stream) {
   const int slots = p.tokens * p.topk;
-  const int most = slots < p.num_groups ? slots : p.num_groups;
-  auto* up = slots <= kWaveSlots ? few_up_kernel<FOUR, true> : few_up_kernel<FOUR, false>;
-  const hipError_t e = launch_kernel(up, dim3((unsigned)strips<FOUR>(p.inter), (unsigned)most), dim3(64 * kUpWaves),
+  const int64_t most = slots < p.num_groups ? slots : p.num_groups, n = strips<FOUR>(p.inter);
+  // several strips a workgroup where there are plenty of workgroups
+  int64_t each = n * most / kUpGroups;
+  each = each < 1 ? 1 : each > 8 ? 8 : each;
+  p.strips_each = (int32_t)each;
+  auto* up = slots <= 64 ? few_up_kernel<FOUR, true> : few_up_kernel<FOUR, false>;
+  const hipError_t e = launch_kernel(up, dim3((unsigned)((n + each - 1) / each), (unsigned)most), dim3(64 * kUpWaves),
                                      stream, p);
   if (e != hipSuccess) return e;
   auto* down = p.tokens <= 16 ? few_down_kernel<FOUR, 16> : few_down_kernel<FOUR, kMaxTokens>;

@@ -23,7 +23,7 @@ def run(name, defaults, case):
 
 BOTH = [(dict(x=0), 1), (dict(ids=0), 1), (dict(w13=0), 1), (dict(w2=0), 1), (dict(out=0), 1), (dict(ws=0), 1),
         (dict(tokens=-1), 2), (dict(topk=0), 2), (dict(hidden=0), 2), (dict(inter=0), 2), (dict(hidden=4), 2),
-        (dict(hidden=(1 << 20) + 32), 2), (dict(inter=1 << 20), 2), (dict(hidden=1 << 17, inter=1 << 13), 2),
+        (dict(hidden=(1 << 20) + 32), 2), (dict(inter=1 << 20), 2), (dict(hidden=1 << 16, inter=1 << 13), 2),
         (dict(x=A + 8), 3), (dict(w13=A + 8), 3), (dict(w2=A + 8), 3), (dict(out=A + 8), 3), (dict(ws=A + 8), 3),
         (dict(ids=A + 2), 3), (dict(wt=A + 2), 3), (dict(dt=2), 4), (dict(dt=-1), 4), (dict(e=0), 5), (dict(e=2049), 5),
         (dict(tokens=65), 5), (dict(tokens=64, topk=17), 5), (dict(tokens=1, topk=1025), 5), (dict(tokens=1 << 62), 5)]
