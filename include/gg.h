@@ -837,7 +837,7 @@ gg_status gg_fp4_masked_forward(const void* x, const void* x_scales,
  * and down products over a few rows of each expert).
  */
 #define GG_FEW_TOKENS_MAX 64
-#define GG_FEW_SLOTS_MAX 1024
+#define GG_FEW_SLOTS_MAX 512
 int64_t gg_moe_few_tokens_workspace_bytes(int64_t tokens, int32_t topk,
                                           int64_t inter, int32_t num_groups);
 gg_status gg_moe_few_tokens(const void* x, const int32_t* expert_of_slot,

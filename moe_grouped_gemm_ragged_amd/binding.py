@@ -1247,7 +1247,7 @@ def fp4_masked_forward(x, x_scales, w, w_scales, masked_m, out=None, out_dtype=N
 # ---------------------------------------------------------------------------
 
 FEW_TOKENS_MAX = 64
-FEW_SLOTS_MAX = 1024
+FEW_SLOTS_MAX = 512
 
 
 def moe_few_tokens_workspace_bytes(tokens, topk, inter, num_groups) -> int:

@@ -24,16 +24,30 @@
 //                same 8 rows at the next values of the reduction, and so are
 //                its columns 8..15: two of its four quarters count
 //
-// A compute unit takes in 25 GB/s of weights from memory, whatever it has in
-// flight, so what counts is that all 256 have the same share: hence strips of
-// 8 rows (of 16, one token's 8 experts, 2048 x 768: up 15.0 us for
-// UP_TOKEN, down 12.0 for DOWN_TOKEN; 23 tokens: down 99 for DOWN_BATCH).
+// A compute unit takes in about 25 GB/s of weights from memory, whatever it has
+// in flight, so what counts is that all 256 have the same share: hence strips of
+// 8 rows (128 experts, hidden 2048, inter 768, bf16, 23 tokens to 8 each: down
+// 61 us, with strips of 16 rows 99; one token 6.9 against 12.2).  The address
+// unit takes 16 bytes of 4 lanes a cycle, used or not: x goes through LDS in the
+// up kernel (4 tokens, 64 experts, 7168 x 2048 in 4 bits: 114 us, loaded by
+// every lane 151), and no load is issued past a wave's last step (one token:
+// up 14.4 us against 16.7, down 6.8 against 8.8).  Small workgroups, 4 of up and
+// 2 of down a compute unit, fill each other's beginnings and ends (up with 8
+// waves 120, 15.0 and 11.8 us where 4 take 113, 13.0 and 7.7; down with 16
+// waves 77 us where 8 take 69).
+//
+// Reached, one token 13.0 + 6.9 us (75 MB; 4 bits 7.7 + 5.3, 20 MB), 23 tokens
+// 111 + 60 us (921 MB: 5.4 TB/s), 4 tokens of the wide 4-bit layer 102 + 69 us
+// (620 MB: 3.6 TB/s: the conversions and rows' operands of 4-bit steps beside
+// the same latencies).  Between the two kernels lies 1.1 us.
 //
 // Which experts are reached, and by whom, a workgroup's first wave finds from
 // the expert ids; the first workgroup of each expert leaves it in the workspace
 // for the down kernel.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
+
+#include <type_traits>
 
 #include "gg_fp4.h"
 #include "gg_internal.h"
@@ -49,8 +63,9 @@ constexpr int kMaxTokens = kFewTokensMax;
 constexpr int kMaxSlots = kFewSlotsMax;
 constexpr int kWaveSlots = 64;                // slots that a wave holds, one a lane
 constexpr int kStrip = 8;                     // weight rows of a strip
-constexpr int kUpWaves = 8, kDownWaves = 16;
+constexpr int kUpWaves = 4, kDownWaves = 8;
 constexpr int kPitch = 2 * kStrip + 1;        // floats between a token's sums in LDS
+constexpr int kRowBytes = 30 << 10;           // x rows of an up workgroup's tokens in LDS, where they fit
 constexpr int kUpGroups = 4096;               // up workgroups from which on each takes several strips
 constexpr int kQuad = 4;                      // tokens of a down product: four columns each
 constexpr uint32_t kOutside = 0x80000000u;    // an offset past every range here
@@ -156,7 +171,7 @@ struct Reader {
     } else {
 #pragma unroll
       for (int j = 0; j < 2; ++j)
-        r.v[j] = load_range(s.w, inside(step, j) ? l.w + 128u * half + 64u * j : kOutside, 2 * kValues * step);
+        r.v[j] = load_range(s.w, (inside(step, j) ? l.w + 128u * half : kOutside) + 64u * j, 2 * kValues * step);
     }
   }
   // The rows' operands: bf16 rows; `at` is the offset of this lane's row's
@@ -165,7 +180,7 @@ struct Reader {
                                        u32x4r (&v)[kOperands]) const {
 #pragma unroll
     for (int j = 0; j < kOperands; ++j)
-      v[j] = load_range(rs, inside(step, j) ? at + 2u * (uint32_t)Step<FOUR>::at(0, j) : kOutside,
+      v[j] = load_range(rs, (inside(step, j) ? at : kOutside) + 2u * (uint32_t)Step<FOUR>::at(0, j),
                         base + 2 * kValues * step);
   }
 };
@@ -233,12 +248,13 @@ __device__ __forceinline__ uint64_t lane_value64(uint64_t v, int lane) {
 // their place.  Whole rounds in the loop, the rest after it: an issue that may
 // be skipped in the loop would make the compiler wait for all loads on every
 // path, and a load out of range costs as much of the address unit's time as
-// any other.
-template <int kAhead, typename Issue, typename Use>
-__device__ __forceinline__ void pipelined(int n, const Issue& issue, const Use& use) {
+// any other.  start() comes between the first issues and the first use.
+template <int kAhead, typename Issue, typename Use, typename Start>
+__device__ __forceinline__ void pipelined(int n, const Issue& issue, const Use& use, const Start& start) {
 #pragma unroll
   for (int a = 0; a < kAhead; ++a)
     if (a < n) issue(a, a);
+  start();
   int i = 0;
   for (; i + 2 * kAhead <= n; i += kAhead) {
 #pragma unroll
@@ -257,14 +273,38 @@ __device__ __forceinline__ void pipelined(int n, const Issue& issue, const Use& 
     if (i + kAhead + a < n) use(a, i + kAhead + a);
 }
 
-// The reduction of one strip over this wave's steps, for up to 16 BLOCKS
-// tokens.
+// The reduction of one strip over this wave's steps, for up to 16 tokens whose
+// rows are in LDS: row i at pitch i, zeros from p.hidden on to the last step's
+// end.  fill() puts them there (and waits for all waves), once the first weights
+// are on their way.  Columns without a token repeat the last one's.
+template <bool FOUR, typename Fill>
+__device__ __forceinline__ void up_steps_lds(const Few& p, const Strip<FOUR>& s, const Lane<FOUR>& l, const uint8_t* x,
+                                             uint32_t pitch, int found, int wave, int col, int q, f32x4f& acc,
+                                             const Fill& fill) {
+  constexpr int kAhead = FOUR ? 6 : 4;
+  const Reader<FOUR, 1> rd(p.hidden, col, q);
+  const uint8_t* const row = x + (uint32_t)(col < found ? col : found - 1) * pitch + 2 * rd.first;
+  Raw<FOUR> w[kAhead];
+  auto issue = [&](int a, int i) __attribute__((always_inline)) {
+    rd.weights(s, l, false, wave + kUpWaves * i, w[a]);
+  };
+  auto use = [&](int a, int i) __attribute__((always_inline)) {
+    const uint8_t* const from = row + (uint32_t)(2 * Reader<FOUR, 1>::kValues) * (uint32_t)(wave + kUpWaves * i);
+#pragma unroll
+    for (int j = 0; j < Step<FOUR>::kOperands; ++j) {
+      const u32x4r v = *reinterpret_cast<const u32x4r*>(from + 2 * Step<FOUR>::at(0, j));
+      acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(operand<FOUR>(w[a], j), __builtin_bit_cast(bf16x8f, v), acc, 0, 0, 0);
+    }
+  };
+  pipelined<kAhead>((rd.steps() - wave + kUpWaves - 1) / kUpWaves, issue, use, fill);
+}
+
+// The same for up to 32 tokens, whose rows are loaded with the weights.
 template <bool FOUR, int BLOCKS>
 __device__ __forceinline__ void up_steps(const Few& p, const Strip<FOUR>& s, const Lane<FOUR>& l, const int32_t* tokens,
-                                         int found, int wave, int col, int q, f32x4f (&acc)[4]) {
-  constexpr int kAhead = BLOCKS == 1 ? 4 : BLOCKS == 2 ? 2 : 1;
+                                         int found, int wave, int col, int q, f32x4f* acc) {
+  constexpr int kAhead = BLOCKS == 1 ? 2 : 1;
   const Reader<FOUR, 1> rd(p.hidden, col, q);
-  const int steps = rd.steps();
   const __amdgpu_buffer_rsrc_t xs = range(p.x, (int64_t)p.tokens * p.hidden * 2);
   uint32_t xat[BLOCKS];
 #pragma unroll
@@ -287,7 +327,7 @@ __device__ __forceinline__ void up_steps(const Few& p, const Strip<FOUR>& s, con
         acc[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wo, __builtin_bit_cast(bf16x8f, x[a][b][j]), acc[b], 0, 0, 0);
     }
   };
-  pipelined<kAhead>((steps - wave + kUpWaves - 1) / kUpWaves, issue, use);
+  pipelined<kAhead>((rd.steps() - wave + kUpWaves - 1) / kUpWaves, issue, use, [] {});
 }
 
 // SMALL: at most 64 slots.
@@ -301,6 +341,7 @@ __global__ __launch_bounds__(64 * kUpWaves, 4) void few_up_kernel(Few p) {
   __shared__ float s_share[kMaxTokens];
   __shared__ int32_t s_info[3];             // their number, the first one's workspace row, the expert
   __shared__ float s_sum[kUpWaves][16][kPitch];
+  __shared__ __attribute__((aligned(16))) uint8_t s_x[kRowBytes];
   const int tid = threadIdx.x, lane = tid & 63, wave = wave_index();
   const int slots = p.tokens * p.topk;
   const int d = blockIdx.y;
@@ -424,6 +465,28 @@ __global__ __launch_bounds__(64 * kUpWaves, 4) void few_up_kernel(Few p) {
   if (tid < found && p.share) share = p.share[s_slot[tid]];
 
   const int col = lane & 15, q = lane >> 4;
+  // x's rows: 16 bytes a load, zeros after them
+  constexpr int kRowLoads = 2;                 // of each thread, ahead of the weights (the rest after them)
+  const uint32_t per = (uint32_t)(Reader<FOUR, 1>(p.hidden, col, q).steps() * Reader<FOUR, 1>::kValues / 8);
+  const uint32_t pitch = 16u * per + 64u;      // (rows a quarter of the banks apart)
+  const uint32_t all = per * (uint32_t)found;
+  const bool in_lds = found <= 16 && (uint64_t)pitch * (uint32_t)found <= (uint64_t)kRowBytes;
+  u32x4r xv[kRowLoads];
+  auto get_x = [&](int m) {
+    const uint32_t c = (uint32_t)(tid + 64 * kUpWaves * m);
+    u32x4r v = {0u, 0u, 0u, 0u};
+    if (c < all && 8u * (c % per) < (uint32_t)p.hidden)
+      v = rows::load16(p.x + (int64_t)s_token[c / per] * p.hidden + 8u * (c % per));
+    return v;
+  };
+  auto put_x = [&](int m, const u32x4r& v) {
+    const uint32_t c = (uint32_t)(tid + 64 * kUpWaves * m);
+    if (c < all) *reinterpret_cast<u32x4r*>(s_x + c / per * pitch + 16u * (c % per)) = v;
+  };
+  if (in_lds) {
+#pragma unroll
+    for (int m = 0; m < kRowLoads; ++m) xv[m] = get_x(m);
+  }
   const int n = (int)strips<FOUR>(p.inter);
   const int block = p.strips_each == 1 ? strip_of(blockIdx.x, gridDim.x) : (int)blockIdx.x;
   for (int z = 0; z < p.strips_each; ++z) {
@@ -436,9 +499,23 @@ __global__ __launch_bounds__(64 * kUpWaves, 4) void few_up_kernel(Few p) {
     f32x4f acc[4];
 #pragma unroll
     for (int b = 0; b < 4; ++b) acc[b] = f32x4f{0.f, 0.f, 0.f, 0.f};
-    if (found <= 16) up_steps<FOUR, 1>(p, s, l, s_token, found, wave, col, q, acc);
-    else if (found <= 32) up_steps<FOUR, 2>(p, s, l, s_token, found, wave, col, q, acc);
-    else up_steps<FOUR, 4>(p, s, l, s_token, found, wave, col, q, acc);
+    if (in_lds) {
+      up_steps_lds<FOUR>(p, s, l, s_x, pitch, found, wave, col, q, acc[0], [&] {
+        if (z > 0) return;
+#pragma unroll
+        for (int m = 0; m < kRowLoads; ++m) put_x(m, xv[m]);
+        for (int m = kRowLoads; 64u * kUpWaves * m < all; ++m) put_x(m, get_x(m));
+        // (the weights stay in flight)
+        __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0)
+        asm volatile("s_barrier" ::: "memory");
+      });
+    } else if (found <= 16) {
+      up_steps<FOUR, 1>(p, s, l, s_token, found, wave, col, q, acc);
+    } else {
+      up_steps<FOUR, 2>(p, s, l, s_token, found, wave, col, q, acc);
+      // (beyond 32 the weights are read twice)
+      if (found > 32) up_steps<FOUR, 2>(p, s, l, s_token + 32, found - 32, wave, col, q, acc + 2);
+    }
     if (z == 0 && tid < found) {
       if (s_more[tid] && p.share) {              // the token's other slots that name the expert
         for (int j = s_slot[tid] + 1; j < (s_token[tid] + 1) * p.topk; ++j)
@@ -493,14 +570,11 @@ __global__ __launch_bounds__(64 * kDownWaves) void few_down_kernel(Few p) {
   const int tid = threadIdx.x, lane = tid & 63, wave = wave_index();
   const int slots = p.tokens * p.topk;
   const int most = slots < p.num_groups ? slots : p.num_groups;
-  // Reached experts, one a lane (loaded before their number is known), the next
-  // 64 when a wave gets there.
+  // Reached experts, one a lane: the first 64 before their number is known, and
+  // where that is not enough the wave's own.  (None is loaded in the loop: a load
+  // that may be skipped there would make it wait for all.)
   Reached mine = {0, 0, 0};
-  int have = 0;
-  auto fetch = [&](int first) {
-    have = first;
-    if (first + lane < most) mine = p.reached[first + lane];
-  };
+  if (lane < most) mine = p.reached[lane];
   const int strip = strip_of(blockIdx.x, gridDim.x);
   const int col = lane & 15, q = lane >> 4;
   const bool second = col >= 8;
@@ -515,41 +589,42 @@ __global__ __launch_bounds__(64 * kDownWaves) void few_down_kernel(Few p) {
   const uint32_t act_at = (uint32_t)((2 * member + ((col >> 2) & 1)) * k + rd.first) * 2u;
   for (int i = lane; i < TOKENS * kStrip / 4; i += 64)
     reinterpret_cast<f32x4f*>(&s_out[wave][0][0])[i] = f32x4f{0.f, 0.f, 0.f, 0.f};
-  fetch(0);
   const int reached = __builtin_amdgcn_readfirstlane(*p.count);
 
   // The reached experts' steps, one expert after the other; a wave takes an
-  // equal run of them.
-  const int items = reached * steps;
-  const int end = (int)((int64_t)items * (wave + 1) / kDownWaves);
-  struct Item {
-    int expert, base, step;
-    uint64_t tokens;
-  };
-  const int begin = (int)((int64_t)items * wave / kDownWaves);
+  // equal run of them (of whole experts where there are many: at most 64).
+  static_assert(kMaxSlots <= 64 * kDownWaves, "a wave holds its experts one a lane");
+  const bool whole = reached >= 256;
+  const int units = whole ? reached : reached * steps, unit = whole ? steps : 1;
+  const int begin = units * wave / kDownWaves * unit, end = units * (wave + 1) / kDownWaves * unit;
   int d = begin / steps, step = begin - d * steps;
-  auto next = [&]() {
-    if (d - have >= 64) fetch(d & ~63);
-    Item i;
-    i.expert = __builtin_amdgcn_readlane(mine.expert, d & 63);
-    i.base = __builtin_amdgcn_readlane(mine.base, d & 63);
-    i.tokens = lane_value64(mine.tokens, d & 63);
-    i.step = step;
-    if (++step == steps) {
-      step = 0;
-      ++d;
-    }
-    return i;
-  };
-  constexpr int kAhead = 4;
+  if (reached > 64) {
+    if (d + lane < reached) mine = p.reached[d + lane];
+    d = 0;
+  }
+  constexpr int kAhead = FOUR ? 3 : 4;
   Raw<FOUR> w[kAhead];
   u32x4r v[kAhead][Step<FOUR>::kOperands];
-  Item ahead[kAhead];
+  int ahead[kAhead];          // the lane of the item's expert
+  // What the next item is loaded with; only the steps change from item to item of
+  // an expert.
+  Strip<FOUR> strip_w(p.down, 0, row0, p.hidden - row0);
+  uint32_t act_lane = kOutside;
+  int act_base = 0, from = -1, issue_d = d, issue_step = step;
   auto issue = [&](int a, int) __attribute__((always_inline)) {
-    const Item i = ahead[a] = next();
-    const int found = __popcll(i.tokens);
-    rd.rows(acts, member < found ? act_at : kOutside, 4 * i.base * k, i.step, v[a]);
-    rd.weights(Strip<FOUR>(p.down, i.expert, row0, p.hidden - row0), l, second, i.step, w[a]);
+    if (issue_d != from) {
+      from = issue_d;
+      strip_w = Strip<FOUR>(p.down, __builtin_amdgcn_readlane(mine.expert, from), row0, p.hidden - row0);
+      act_base = 4 * __builtin_amdgcn_readlane(mine.base, from) * k;
+      act_lane = member < __popcll(lane_value64(mine.tokens, from)) ? act_at : kOutside;
+    }
+    ahead[a] = from;
+    rd.rows(acts, act_lane, act_base, issue_step, v[a]);
+    rd.weights(strip_w, l, second, issue_step, w[a]);
+    if (++issue_step == steps) {
+      issue_step = 0;
+      ++issue_d;
+    }
   };
   auto multiply = [&](const Raw<FOUR>& wr, const u32x4r (&vr)[Step<FOUR>::kOperands], f32x4f c)
       __attribute__((always_inline)) {
@@ -575,25 +650,31 @@ __global__ __launch_bounds__(64 * kDownWaves) void few_down_kernel(Few p) {
     }
   };
   f32x4f part = {0.f, 0.f, 0.f, 0.f};
-  int expert = -1;
-  uint64_t tokens = 0;
-  auto use = [&](int a, int) __attribute__((always_inline)) {
-    const Item i = ahead[a];
-    if (i.expert != expert) {
+  int current = d;
+  uint64_t tokens = end > begin ? lane_value64(mine.tokens, d) : 0ull;
+  auto use = [&](auto many, int a, int i) __attribute__((always_inline)) {
+    if (ahead[a] != current) {
       add(part, tokens, 0);
       part = f32x4f{0.f, 0.f, 0.f, 0.f};
-      expert = i.expert;
-      tokens = i.tokens;
+      current = ahead[a];
+      tokens = lane_value64(mine.tokens, current);
     }
     part = multiply(w[a], v[a], part);
-    const int found = __popcll(i.tokens);
-    for (int b = 1; kQuad * b < found; ++b) {
-      u32x4r more[Step<FOUR>::kOperands];
-      rd.rows(acts, kQuad * b + member < found ? act_at : kOutside, 4 * (i.base + kQuad * b) * k, i.step, more);
-      add(multiply(w[a], more, f32x4f{0.f, 0.f, 0.f, 0.f}), i.tokens, b);
+    if constexpr (decltype(many)::value) {
+      const int found = __popcll(tokens), base = __builtin_amdgcn_readlane(mine.base, current);
+      for (int b = 1; kQuad * b < found; ++b) {
+        u32x4r more[Step<FOUR>::kOperands];
+        rd.rows(acts, kQuad * b + member < found ? act_at : kOutside, 4 * (base + kQuad * b) * k, (step + i) % steps, more);
+        add(multiply(w[a], more, f32x4f{0.f, 0.f, 0.f, 0.f}), tokens, b);
+      }
     }
   };
-  pipelined<kAhead>(end - begin, issue, use);
+  // (without an expert of more tokens the loop holds no loads under a condition)
+  const int last = d + (step + end - begin - 1) / steps;
+  if (__ballot(lane >= d && lane <= last && __popcll(mine.tokens) > kQuad) == 0ull)
+    pipelined<kAhead>(end - begin, issue, [&](int a, int i) { use(std::false_type(), a, i); }, [] {});
+  else
+    pipelined<kAhead>(end - begin, issue, [&](int a, int i) { use(std::true_type(), a, i); }, [] {});
   add(part, tokens, 0);
   __syncthreads();
   for (int o = tid; o < p.tokens * kStrip; o += 64 * kDownWaves) {

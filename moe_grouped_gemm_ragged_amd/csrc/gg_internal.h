@@ -79,7 +79,7 @@ hipError_t launch_fp4_pack_scales(int layout, const void* src, int64_t ld_src, c
 // hidden] and w2 [E, hidden, inter] in bf16, or codes with packed scales.  share
 // may be null.  tokens <= kFewTokensMax, tokens * topk <= kFewSlotsMax.
 constexpr int kFewTokensMax = 64;
-constexpr int kFewSlotsMax = 1024;
+constexpr int kFewSlotsMax = 512;
 int64_t few_tokens_workspace(int64_t slots, int64_t inter, int32_t E);
 hipError_t launch_few_tokens(bool four, const void* x, const int32_t* experts, const float* share, const void* w13,
                              const void* s13, const void* w2, const void* s2, void* out, bool out_f32, void* workspace,
