@@ -58,31 +58,55 @@ __device__ __forceinline__ uint32_t quad_max(uint32_t v) {
   return o > v ? o : v;
 }
 
-// The codes of this lane's 8 values and its block's scale byte.  All 4 lanes
-// of a quad call it together; they hold one block.  Dividing by a power of
-// two is exact (2^-126 s <= |v| or the quotient is below half a step), and
-// the conversion rounds to nearest even.
-__device__ __forceinline__ uint32_t quantise4(const float (&v)[8], int& byte) {
+// The largest magnitude of a lane's 8 values, as fp32 bits: the order of
+// magnitudes is that of their bits, infinity and NaN on top.
+__device__ __forceinline__ uint32_t magnitude(const rows::u32x4r& q) {      // bf16
+  typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+  u16x2 m = __builtin_bit_cast(u16x2, q[0] & 0x7FFF7FFFu);
+#pragma unroll
+  for (int e = 1; e < 4; ++e) m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, q[e] & 0x7FFF7FFFu));
+  return (uint32_t)(m[0] > m[1] ? m[0] : m[1]) << 16;
+}
+__device__ __forceinline__ uint32_t magnitude(const float (&v)[8]) {
   uint32_t m = 0;
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    // the order of magnitudes is that of their bits, infinity and NaN on top
     const uint32_t a = __builtin_bit_cast(uint32_t, v[e]) & 0x7FFFFFFFu;
     m = a > m ? a : m;
   }
-  m = quad_max(m);
-  if (__builtin_expect(m >= 0x7F800000u, 0)) {
-    byte = 255;
-    return 0u;
-  }
-  byte = scale_byte4(m);
-  const float inv = rows::inverse_scale(byte);
+  return m;
+}
+
+// The conversions divide by a power of two (exact) and round once, to nearest
+// even.  (They take the scale's exponent bits alone.)
+__device__ __forceinline__ uint32_t codes8(const rows::u32x4r& q, float s) {
+  // (pairs by shuffles: a bit cast of a vector's element takes element 0, with
+  // this compiler, whichever is named)
+  typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+  const bf16x8 b = __builtin_bit_cast(bf16x8, q);
   uint32_t w = 0;
-  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[0] * inv, v[1] * inv, 1.0f, 0);
-  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[2] * inv, v[3] * inv, 1.0f, 1);
-  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[4] * inv, v[5] * inv, 1.0f, 2);
-  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[6] * inv, v[7] * inv, 1.0f, 3);
-  return w;
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(w, __builtin_shufflevector(b, b, 0, 1), s, 0);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(w, __builtin_shufflevector(b, b, 2, 3), s, 1);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(w, __builtin_shufflevector(b, b, 4, 5), s, 2);
+  return __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(w, __builtin_shufflevector(b, b, 6, 7), s, 3);
+}
+__device__ __forceinline__ uint32_t codes8(const float (&v)[8], float s) {
+  uint32_t w = 0;
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[0], v[1], s, 0);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[2], v[3], s, 1);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[4], v[5], s, 2);
+  return __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[6], v[7], s, 3);
+}
+
+// The codes of this lane's 8 values and its block's scale byte.  All 4 lanes
+// of a quad call it together; they hold one block.
+template <typename V>
+__device__ __forceinline__ uint32_t quantise4(const V& v, int& byte) {
+  const uint32_t m = quad_max(magnitude(v));
+  const bool bad = m >= 0x7F800000u;
+  byte = bad ? 255 : scale_byte4(m);
+  const uint32_t c = codes8(v, __builtin_bit_cast(float, (uint32_t)byte << 23));
+  return bad ? 0u : c;
 }
 
 }  // namespace fp4

@@ -14,7 +14,13 @@
 // one workgroup assembles in LDS and writes whole, where rows one at a time
 // would write single bytes 1 KB apart.  A row's part of a unit is 512 bytes
 // of bf16 and 128 of codes, 32 lanes with 8 values each; 4 lanes hold a
-// block, so its largest value is two lane exchanges away.  Bound by memory.
+// block, so its largest value is two lane exchanges away.
+//
+// Bound by memory: 65536 rows of 2048 values 74 us (339 MB: 4.6 TB/s; a copy 5.05),
+// back 60 us (5.6 TB/s), 64 x 1536 rows of weights 105 and 104 us, silu of 65536
+// rows to 768 values 52 us (229 MB).  gather, 8192 tokens of 2048 values to 8 of
+// 128 experts: 55 us (33.5 MB in, 71 out, a token read for each of its rows);
+// with a row's slot read by every thread as it needs it 91.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -126,6 +132,12 @@ __device__ __forceinline__ void tile_rows(const S& s, const int32_t* groups, int
   }
 }
 
+__device__ __forceinline__ int64_t uniform64(int64_t v) {
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)v);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)((uint64_t)v >> 32));
+  return (int64_t)((uint64_t)hi << 32 | lo);
+}
+
 struct In {
   const uint16_t* x;         // plain: rows; gather: token rows; silu: gate/up rows of 2 k values
   const int32_t* row_slot;   // gather
@@ -140,6 +152,7 @@ __global__ __launch_bounds__(kThreads) void to4_kernel(In in, const int32_t* gro
                                                        int64_t tiles, uint8_t* codes, uint8_t* scales) {
   __shared__ std::conditional_t<LAYOUT == RAGGED, Tiles, NoTiles> s_tiles;
   __shared__ uint32_t s_sc[kUnitStages * kStageBytes / 2 / 4];     // [stage][half tile]
+  __shared__ int32_t s_token[SRC == GATHER ? kHalf : 1];
   const int tid = threadIdx.x;
   if constexpr (LAYOUT == RAGGED) tiles = decode_tiles(s_tiles, groups, rows, E, tid);
   const int64_t stages = stages4(k);
@@ -147,40 +160,57 @@ __global__ __launch_bounds__(kThreads) void to4_kernel(In in, const int32_t* gro
   const int lane = tid & 31, rsub = tid >> 5;
   uint8_t* const my = reinterpret_cast<uint8_t*>(s_sc) + 512 * (lane >> 4);
   const int q = (lane & 15) >> 2;
-  for (int64_t u = blockIdx.x; u < 2 * tiles * across; u += gridDim.x) {
-    const int64_t th = u / across;
-    const int64_t s0 = (u - th * across) * kUnitStages;
+  // Units in the order of their rows; gather: of their columns, an eighth of that
+  // list to each XCD (workgroup b runs on XCD b mod 8), so that a token's piece
+  // comes from memory once and its other rows find it in the XCD's L2.
+  const int64_t units = 2 * tiles * across;
+  const bool by_xcd = SRC == GATHER && gridDim.x % 8 == 0;
+  const int64_t x = by_xcd ? blockIdx.x % 8 : 0, each = by_xcd ? 8 : 1;
+  const int64_t end = by_xcd ? units * (x + 1) / 8 : units;
+  for (int64_t u = (by_xcd ? units * x / 8 : 0) + blockIdx.x / each; u < end; u += gridDim.x / each) {
+    const int64_t th = SRC == GATHER ? u % (2 * tiles) : u / across;
+    const int64_t s0 = (SRC == GATHER ? u / (2 * tiles) : u - th * across) * kUnitStages;
     const int half = (int)(th & 1);
     int64_t first;
     int valid;
     tile_rows<LAYOUT>(s_tiles, groups, rows, E, th >> 1, first, valid);
     if (valid <= 0) continue;                    // (masked: a tile without rows)
-    valid -= kHalf * half;
-    first += kHalf * half;
+    valid = __builtin_amdgcn_readfirstlane(valid) - kHalf * half;
+    first = uniform64(first) + kHalf * half;
     const int64_t col = s0 * kStage4 + 8 * lane;
+    // (a unit's rows span 2^29 bytes at most: 32-bit offsets from a scalar base)
+    const uint32_t pitch = 2u * (uint32_t)k;
+    const uint8_t* const from =
+        reinterpret_cast<const uint8_t*>(in.x + (SRC == GATHER ? 0 : (SRC == SILU ? 2 : 1) * first * k)) +
+        2 * s0 * kStage4;
+    uint8_t* const to = codes + first * (k / 2) + s0 * kStage4 / 2;
+    const uint32_t lane16 = 16u * (uint32_t)lane;
     s_sc[tid] = 0u;
+    if constexpr (SRC == GATHER) {
+      // the rows' tokens (-1: padding)
+      if (tid < valid && tid < kHalf) {
+        const int32_t slot = in.row_slot[first + tid], t = slot / in.topk;
+        s_token[tid] = slot < 0 || t >= in.tokens ? -1 : t;
+      }
+    }
     __syncthreads();
     if (col < k) {
       constexpr int kAhead = 4;
       for (int r0 = rsub; r0 < valid && r0 < kHalf; r0 += kRowsAtOnce * kAhead) {
         u32x4r g[kAhead], up[SRC == SILU ? kAhead : 1];
-        bool pad[kAhead];
 #pragma unroll
         for (int a = 0; a < kAhead; ++a) {
           const int r = r0 + kRowsAtOnce * a;
-          pad[a] = false;
           g[a] = u32x4r{0u, 0u, 0u, 0u};
           if (r < valid && r < kHalf) {
             if constexpr (SRC == PLAIN) {
-              g[a] = load16(in.x + (first + r) * k + col);
+              g[a] = load16(from + (lane16 + (uint32_t)r * pitch));
             } else if constexpr (SRC == SILU) {
-              g[a] = load16(in.x + (first + r) * 2 * k + col);
-              up[a] = load16(in.x + (first + r) * 2 * k + k + col);
+              g[a] = load16(from + (lane16 + (uint32_t)r * 2u * pitch));
+              up[a] = load16(from + (lane16 + ((uint32_t)r * 2u + 1u) * pitch));
             } else {
-              const int32_t slot = in.row_slot[first + r];
-              const int32_t t = slot / in.topk;
-              pad[a] = slot < 0 || t >= in.tokens;
-              if (!pad[a]) g[a] = load16(in.x + (int64_t)t * k + col);
+              const int32_t t = s_token[r];
+              if (t >= 0) g[a] = load16(from + ((uint64_t)(uint32_t)t * pitch + lane16));
             }
           }
         }
@@ -188,17 +218,19 @@ __global__ __launch_bounds__(kThreads) void to4_kernel(In in, const int32_t* gro
         for (int a = 0; a < kAhead; ++a) {
           const int r = r0 + kRowsAtOnce * a;
           if (r < valid && r < kHalf) {
-            float v[8];
-            unpack8(g[a], v);
+            int byte;
+            uint32_t c;
             if constexpr (SRC == SILU) {
-              float w[8];
+              float v[8], w[8];
+              unpack8(g[a], v);
               unpack8(up[a], w);
 #pragma unroll
               for (int e = 0; e < 8; ++e) v[e] = v[e] * sigmoid(v[e]) * w[e];
+              c = quantise4(v, byte);
+            } else {
+              c = quantise4(g[a], byte);
             }
-            int byte;
-            const uint32_t c = quantise4(v, byte);
-            *reinterpret_cast<uint32_t*>(codes + (first + r) * (k / 2) + col / 2) = c;
+            *reinterpret_cast<uint32_t*>(to + (4u * (uint32_t)lane + (uint32_t)r * (pitch / 4))) = c;
             if ((lane & 3) == 0) my[scale_place(r, q)] = (uint8_t)byte;
           }
         }
