@@ -10,6 +10,7 @@ fails, an exception is raised.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import re
 from typing import Optional
@@ -1093,6 +1094,8 @@ GG_FP4_ACT_MASKED = 1
 GG_FP4_WEIGHT = 2
 
 
+# (sizes of sizes: asked once for each, a small call would spend 2 us of its 15 on them)
+@functools.lru_cache(maxsize=1024)
 def fp4_scale_bytes(layout: int, rows: int, k: int, num_groups: int) -> int:
     """Bytes of packed scales (gg_fp4_scale_bytes)."""
     v = int(load().gg_fp4_scale_bytes(int(layout), int(rows), int(k), int(num_groups)))
@@ -1250,6 +1253,7 @@ FEW_TOKENS_MAX = 64
 FEW_SLOTS_MAX = 512
 
 
+@functools.lru_cache(maxsize=1024)
 def moe_few_tokens_workspace_bytes(tokens, topk, inter, num_groups) -> int:
     v = int(load().gg_moe_few_tokens_workspace_bytes(int(tokens), int(topk), int(inter), int(num_groups)))
     if v < 0:
@@ -1270,27 +1274,33 @@ def _few_tokens(name, x, experts, weights, w13, s13, w2, s2, wdtype, per, out, o
         _shaped(weights, "weights", torch.float32, (tokens, topk), dev)
     _check(w13, "w13", wdtype, 3, dev)
     _check(w2, "w2", wdtype, 3, dev)
-    e, inter = w13.shape[0], w13.shape[1] // 2
-    if w13.shape[1] % 2 or w13.shape[2] * per != hidden or w2.shape[0] != e or w2.shape[1] != hidden or \
-            w2.shape[2] * per != inter:
+    e, rows, width = w13.shape
+    inter = rows // 2
+    if rows % 2 or width * per != hidden or inter % per or w2.shape != (e, hidden, inter // per):
         raise ValueError("shape mismatch between x, w13 and w2")
+    ptrs = (w13.data_ptr(), w2.data_ptr())
     if per == 2:
         if hidden % 32 or inter % 32:
             raise ValueError("hidden and inter must be multiples of 32")
         if s13 is None or s2 is None:
             raise ValueError("w13_scales and w2_scales are required")
-        _packed4(s13, "w13_scales", GG_FP4_WEIGHT, 2 * inter, hidden, e, dev)
+        _packed4(s13, "w13_scales", GG_FP4_WEIGHT, rows, hidden, e, dev)
         _packed4(s2, "w2_scales", GG_FP4_WEIGHT, hidden, inter, e, dev)
+        ptrs = (ptrs[0], s13.data_ptr(), ptrs[1], s2.data_ptr())
     need = moe_few_tokens_workspace_bytes(tokens, topk, inter, e)
     if workspace is None:
         workspace = _shaped(None, "workspace", torch.uint8, (need,), dev)
-    _check(workspace, "workspace", torch.uint8, 1, dev)
-    if workspace.numel() < need:
-        raise ValueError(f"workspace must hold {need} bytes")
-    out = _shaped(out, "out", (out_dtype or torch.bfloat16) if out is None else out.dtype, (tokens, hidden), dev)
-    ws = (_ptr(w13), _ptr(s13), _ptr(w2), _ptr(s2)) if per == 2 else (_ptr(w13), _ptr(w2))
-    _launch(name, dev, _ptr(x), _ptr(experts), _ptr(weights), *ws, _ptr(out), _dtype_code(out.dtype), _ptr(workspace),
-            tokens, topk, hidden, inter, e)
+    else:
+        _check(workspace, "workspace", torch.uint8, 1, dev)
+        if workspace.numel() < need:
+            raise ValueError(f"workspace must hold {need} bytes")
+    if out is None and (out_dtype is None or out_dtype == torch.bfloat16):
+        out, code = torch.empty_like(x), GG_BF16
+    else:
+        out = _shaped(out, "out", out_dtype if out is None else out.dtype, (tokens, hidden), dev)
+        code = _dtype_code(out.dtype)
+    _launch(name, dev, x.data_ptr(), experts.data_ptr(), _ptr(weights), *ptrs, out.data_ptr(), code,
+            workspace.data_ptr(), tokens, topk, hidden, inter, e)
     return out
 
 
