@@ -45,7 +45,7 @@ def pack(codes):
 
 
 def unpack(b):
-    return torch.stack([b & 15, b >> 4], -1).reshape(*b.shape[:-1], -1)
+    return torch.stack([b & 15, b >> 4], -1).flatten(-2)
 
 
 def value(packed, scales):
