@@ -37,8 +37,8 @@
 // waves 77 us where 8 take 69).
 //
 // Reached, one token 13.0 + 6.9 us (75 MB; 4 bits 7.7 + 5.3, 20 MB), 23 tokens
-// 111 + 60 us (921 MB: 5.4 TB/s), 4 tokens of the wide 4-bit layer 102 + 69 us
-// (620 MB: 3.6 TB/s: the conversions and rows' operands of 4-bit steps beside
+// 111 + 60 us (921 MB: 5.4 TB/s), 4 tokens of the wide 4-bit layer 102 + 55 us
+// (620 MB: 3.9 TB/s: the conversions and rows' operands of 4-bit steps beside
 // the same latencies).  Between the two kernels lies 1.1 us.
 //
 // Which experts are reached, and by whom, a workgroup's first wave finds from
@@ -67,6 +67,7 @@ constexpr int kUpWaves = 4, kDownWaves = 8;
 constexpr int kPitch = 2 * kStrip + 1;        // floats between a token's sums in LDS
 constexpr int kRowBytes = 30 << 10;           // x rows of an up workgroup's tokens in LDS, where they fit
 constexpr int kUpGroups = 4096;               // up workgroups from which on each takes several strips
+constexpr unsigned kDownPairs = 512;          // 4-bit down strips from which on a workgroup takes two
 constexpr int kQuad = 4;                      // tokens of a down product: four columns each
 constexpr uint32_t kOutside = 0x80000000u;    // an offset past every range here
 
@@ -506,8 +507,7 @@ __global__ __launch_bounds__(64 * kUpWaves, 4) void few_up_kernel(Few p) {
         for (int m = 0; m < kRowLoads; ++m) put_x(m, xv[m]);
         for (int m = kRowLoads; 64u * kUpWaves * m < all; ++m) put_x(m, get_x(m));
         // (the weights stay in flight)
-        __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0)
-        asm volatile("s_barrier" ::: "memory");
+        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
       });
     } else if (found <= 16) {
       up_steps<FOUR, 1>(p, s, l, s_token, found, wave, col, q, acc);
@@ -563,10 +563,16 @@ __device__ __forceinline__ float half_mirror(float v) {
                             __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0x141, 0xf, 0xf, true));
 }
 
-// TOKENS: at most.
-template <bool FOUR, int TOKENS>
+// TOKENS: at most.  SUB: strips of a workgroup, side by side in their span (4
+// bits): a step's four loads of rows then serve two of weights.  With both and
+// their scales a strip's step costs the address unit 64 clocks instead of 96.  Where
+// every compute unit keeps a workgroup: some 25 experts of 7168 x 2048 69 -> 55 us, 8
+// of them 23.5 -> 21.6, some 40 of 4096 x 1536 49 -> 37; 64 workgroups of 128 strips 4.6 ->
+// 5.5, so fewer than kDownPairs strips keep one each.
+template <bool FOUR, int TOKENS, int SUB>
 __global__ __launch_bounds__(64 * kDownWaves) void few_down_kernel(Few p) {
-  __shared__ __attribute__((aligned(16))) float s_out[kDownWaves][TOKENS][kStrip];     // each wave's sums
+  static_assert(SUB == 1 || FOUR, "bf16 strips do not share a span");
+  __shared__ __attribute__((aligned(16))) float s_out[kDownWaves][SUB * TOKENS][kStrip];     // each wave's sums
   const int tid = threadIdx.x, lane = tid & 63, wave = wave_index();
   const int slots = p.tokens * p.topk;
   const int most = slots < p.num_groups ? slots : p.num_groups;
@@ -575,19 +581,20 @@ __global__ __launch_bounds__(64 * kDownWaves) void few_down_kernel(Few p) {
   // that may be skipped there would make it wait for all.)
   Reached mine = {0, 0, 0};
   if (lane < most) mine = p.reached[lane];
-  const int strip = strip_of(blockIdx.x, gridDim.x);
+  const int strip = SUB * strip_of(blockIdx.x, gridDim.x);
   const int col = lane & 15, q = lane >> 4;
   const bool second = col >= 8;
   const Reader<FOUR, 2> rd(p.inter, col, q);
   const int k = p.inter, steps = rd.steps();
   const int64_t row0 = strip_first<FOUR>(strip);
-  const Lane<FOUR> l(p.down, row0, strip_place<FOUR>(strip, col & 7), q);
+  const Lane<FOUR> l0(p.down, row0, strip_place<FOUR>(strip, col & 7), q);
+  const Lane<FOUR> l1(p.down, row0, strip_place<FOUR>(strip + SUB - 1, col & 7), q);
   const __amdgpu_buffer_rsrc_t acts = range(p.act, (int64_t)slots * 4 * k);
   // columns 0..3 are the bf16 values of 4 of an expert's tokens, 7..4 what those
   // left; 8..15 the same at the step's second half
   const int member = (col & 4) ? 3 - (col & 3) : col & 3;
   const uint32_t act_at = (uint32_t)((2 * member + ((col >> 2) & 1)) * k + rd.first) * 2u;
-  for (int i = lane; i < TOKENS * kStrip / 4; i += 64)
+  for (int i = lane; i < SUB * TOKENS * kStrip / 4; i += 64)
     reinterpret_cast<f32x4f*>(&s_out[wave][0][0])[i] = f32x4f{0.f, 0.f, 0.f, 0.f};
   const int reached = __builtin_amdgcn_readfirstlane(*p.count);
 
@@ -603,7 +610,7 @@ __global__ __launch_bounds__(64 * kDownWaves) void few_down_kernel(Few p) {
     d = 0;
   }
   constexpr int kAhead = FOUR ? 3 : 4;
-  Raw<FOUR> w[kAhead];
+  Raw<FOUR> w[kAhead][SUB];
   u32x4r v[kAhead][Step<FOUR>::kOperands];
   int ahead[kAhead];          // the lane of the item's expert
   // What the next item is loaded with; only the steps change from item to item of
@@ -620,7 +627,8 @@ __global__ __launch_bounds__(64 * kDownWaves) void few_down_kernel(Few p) {
     }
     ahead[a] = from;
     rd.rows(acts, act_lane, act_base, issue_step, v[a]);
-    rd.weights(strip_w, l, second, issue_step, w[a]);
+    rd.weights(strip_w, l0, second, issue_step, w[a][0]);
+    if constexpr (SUB == 2) rd.weights(strip_w, l1, second, issue_step, w[a][1]);
     if (++issue_step == steps) {
       issue_step = 0;
       ++issue_d;
@@ -637,35 +645,42 @@ __global__ __launch_bounds__(64 * kDownWaves) void few_down_kernel(Few p) {
   // expert's product is one of its own, so that a weight that is not finite
   // reaches the expert's own tokens only.)  Lanes 0..31 hold the first half's
   // rows in columns 0..7, lanes 32..63 the second's in 8..15.
-  auto add = [&](f32x4f part, uint64_t tokens, int b) {
+  auto add = [&](f32x4f part, uint64_t tokens, int b, int sub) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) part[e] += half_mirror(part[e]);
     const int i = kQuad * b + (col & 3);
     if ((col & 4) == 0 && i < __popcll(tokens)) {
       uint64_t left = tokens;
       for (int z = 0; z < i; ++z) left &= left - 1ull;
-      f32x4f* to = reinterpret_cast<f32x4f*>(&s_out[wave][__ffsll((unsigned long long)left) - 1][4 * (q & 1)]);
+      f32x4f* to = reinterpret_cast<f32x4f*>(&s_out[wave][sub * TOKENS + __ffsll((unsigned long long)left) - 1][4 * (q & 1)]);
       if (q < 2 && !second) *to = *to + part;
       if (q >= 2 && second) *to = *to + part;
     }
   };
-  f32x4f part = {0.f, 0.f, 0.f, 0.f};
+  f32x4f part[SUB];
+#pragma unroll
+  for (int z = 0; z < SUB; ++z) part[z] = f32x4f{0.f, 0.f, 0.f, 0.f};
   int current = d;
   uint64_t tokens = end > begin ? lane_value64(mine.tokens, d) : 0ull;
   auto use = [&](auto many, int a, int i) __attribute__((always_inline)) {
     if (ahead[a] != current) {
-      add(part, tokens, 0);
-      part = f32x4f{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int z = 0; z < SUB; ++z) {
+        add(part[z], tokens, 0, z);
+        part[z] = f32x4f{0.f, 0.f, 0.f, 0.f};
+      }
       current = ahead[a];
       tokens = lane_value64(mine.tokens, current);
     }
-    part = multiply(w[a], v[a], part);
+#pragma unroll
+    for (int z = 0; z < SUB; ++z) part[z] = multiply(w[a][z], v[a], part[z]);
     if constexpr (decltype(many)::value) {
       const int found = __popcll(tokens), base = __builtin_amdgcn_readlane(mine.base, current);
       for (int b = 1; kQuad * b < found; ++b) {
         u32x4r more[Step<FOUR>::kOperands];
         rd.rows(acts, kQuad * b + member < found ? act_at : kOutside, 4 * (base + kQuad * b) * k, (step + i) % steps, more);
-        add(multiply(w[a], more, f32x4f{0.f, 0.f, 0.f, 0.f}), tokens, b);
+#pragma unroll
+        for (int z = 0; z < SUB; ++z) add(multiply(w[a][z], more, f32x4f{0.f, 0.f, 0.f, 0.f}), tokens, b, z);
       }
     }
   };
@@ -675,15 +690,16 @@ __global__ __launch_bounds__(64 * kDownWaves) void few_down_kernel(Few p) {
     pipelined<kAhead>(end - begin, issue, [&](int a, int i) { use(std::false_type(), a, i); }, [] {});
   else
     pipelined<kAhead>(end - begin, issue, [&](int a, int i) { use(std::true_type(), a, i); }, [] {});
-  add(part, tokens, 0);
+#pragma unroll
+  for (int z = 0; z < SUB; ++z) add(part[z], tokens, 0, z);
   __syncthreads();
-  for (int o = tid; o < p.tokens * kStrip; o += 64 * kDownWaves) {
-    const int t = o / kStrip, i = o % kStrip;
-    const int64_t c = row0 + strip_place<FOUR>(strip, i);
+  for (int o = tid; o < SUB * p.tokens * kStrip; o += 64 * kDownWaves) {
+    const int sub = o / kStrip % SUB, t = o / (SUB * kStrip), i = o % kStrip;
+    const int64_t c = row0 + strip_place<FOUR>(strip + sub, i);
     if (c >= p.hidden) continue;
     float sum = 0.f;
 #pragma unroll
-    for (int z = 0; z < kDownWaves; ++z) sum += s_out[z][t][i];
+    for (int z = 0; z < kDownWaves; ++z) sum += s_out[z][sub * TOKENS + t][i];
     if (p.out_f32) static_cast<float*>(p.out)[(int64_t)t * p.hidden + c] = sum;
     else static_cast<__bf16*>(p.out)[(int64_t)t * p.hidden + c] = (__bf16)sum;
   }
@@ -701,8 +717,15 @@ hipError_t launch_four(Few p, hipStream_t stream) {
   const hipError_t e = launch_kernel(up, dim3((unsigned)((n + each - 1) / each), (unsigned)most), dim3(64 * kUpWaves),
                                      stream, p);
   if (e != hipSuccess) return e;
-  auto* down = p.tokens <= 16 ? few_down_kernel<FOUR, 16> : few_down_kernel<FOUR, kMaxTokens>;
-  return launch_kernel(down, dim3((unsigned)strips<FOUR>(p.hidden)), dim3(64 * kDownWaves), stream, p);
+  auto* down = p.tokens <= 16 ? few_down_kernel<FOUR, 16, 1> : few_down_kernel<FOUR, kMaxTokens, 1>;
+  unsigned groups = (unsigned)strips<FOUR>(p.hidden);
+  if constexpr (FOUR) {
+    if (groups >= kDownPairs) {
+      down = p.tokens <= 16 ? few_down_kernel<FOUR, 16, 2> : few_down_kernel<FOUR, kMaxTokens, 2>;
+      groups /= 2;
+    }
+  }
+  return launch_kernel(down, dim3(groups), dim3(64 * kDownWaves), stream, p);
 }
 
 // The workspace: the count (16 bytes), the reached experts, the rows.

@@ -102,6 +102,18 @@ def test_layer(four, tokens, topk, experts, hidden, inter, dtype):
 
 
 @pytest.mark.parametrize("four", [False, True])
+@pytest.mark.parametrize("tokens,topk,hidden", [(1, 2, 4096), (6, 3, 4128), (40, 2, 4128), (64, 4, 4224)])
+def test_wide(four, tokens, topk, hidden):
+    """Rows enough for two strips a workgroup in the down product of 4 bits; a
+    last span that ends after 32 rows."""
+    device()
+    layer = Layer(four, 5, hidden, 160, 7)
+    x, ids, weights = inputs(tokens, tokens, topk, 5, hidden, drop=0.1 if tokens > 8 else 0.0)
+    say("few tokens: wide", four, tokens, topk, hidden)
+    layer.check(layer(x, ids, weights), x, ids, weights, "wide")
+
+
+@pytest.mark.parametrize("four", [False, True])
 def test_slots(four):
     """No weights; every token one expert; an expert named twice; all dropped."""
     device()
