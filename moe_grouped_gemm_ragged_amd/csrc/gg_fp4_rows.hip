@@ -16,10 +16,10 @@
 // of bf16 and 128 of codes, 32 lanes with 8 values each; 4 lanes hold a
 // block, so its largest value is two lane exchanges away.
 //
-// Bound by memory: 65536 rows of 2048 values 74 us (339 MB: 4.6 TB/s; a copy 5.05),
-// back 60 us (5.6 TB/s), 64 x 1536 rows of weights 105 and 104 us, silu of 65536
-// rows to 768 values 52 us (229 MB).  gather, 8192 tokens of 2048 values to 8 of
-// 128 experts: 55 us (33.5 MB in, 71 out, a token read for each of its rows);
+// Bound by memory: 65536 rows of 2048 values 72 us (339 MB: 4.7 TB/s; a copy 5.05),
+// back 61 us (5.5 TB/s), 64 x 1536 rows of weights 99 and 96 us, silu of 65536
+// rows to 768 values 53 us (229 MB).  gather, 8192 tokens of 2048 values to 8 of
+// 128 experts: 47 us (33.5 MB in, 71 out, a token read for each of its rows);
 // with a row's slot read by every thread as it needs it 91.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -333,9 +333,15 @@ __global__ __launch_bounds__(kThreads) void pack4_kernel(const uint8_t* src, int
   }
 }
 
-int grid_for(int64_t tiles, int64_t k, int num_cus) {
+// Workgroups a compute unit.  To 4 bits 6, as many as its registers hold at once but
+// for silu's 5 (8: the last begin when others end, and have as much to do: gather 55
+// us against 47, weights 105 against 99; 4: 57 and 99).  Back 5: weights 96 us, with 8
+// of them 104, with 6 105; 65536 rows 61.5, 60 and 61.
+constexpr int kToGroups = 6, kFromGroups = 5;
+
+int grid_for(int64_t tiles, int64_t k, int num_cus, int each) {
   const int64_t units = 2 * tiles * ((stages4(k) + kUnitStages - 1) / kUnitStages);
-  const int64_t most = 8 * (int64_t)num_cus;
+  const int64_t most = each * (int64_t)num_cus;
   return (int)(units < most ? units : most);
 }
 
@@ -344,8 +350,8 @@ hipError_t to4(const In& in, const int32_t* groups, int64_t rows, int64_t k, int
                int num_cus, hipStream_t stream) {
   const int64_t tiles = fp4_scale_tiles(LAYOUT, rows, E);
   auto* kernel = to4_kernel<LAYOUT, PLAIN>;
-  return launch_kernel(kernel, dim3(grid_for(tiles, k, num_cus)), dim3(kThreads), stream, in, groups, rows, k, E,
-                       tiles, static_cast<uint8_t*>(codes), static_cast<uint8_t*>(scales));
+  return launch_kernel(kernel, dim3(grid_for(tiles, k, num_cus, kToGroups)), dim3(kThreads), stream, in, groups, rows,
+                       k, E, tiles, static_cast<uint8_t*>(codes), static_cast<uint8_t*>(scales));
 }
 
 }  // namespace
@@ -372,8 +378,9 @@ hipError_t launch_fp4_gather_rows(const void* src, int64_t tokens, int64_t k, co
   if (rows_cap == 0) return hipSuccess;
   const In in = {static_cast<const uint16_t*>(src), row_slot, topk, tokens};
   const int64_t tiles = fp4_scale_tiles(RAGGED, rows_cap, E);
-  return launch_kernel(to4_kernel<RAGGED, GATHER>, dim3(grid_for(tiles, k, num_cus)), dim3(kThreads), stream, in, offs,
-                       rows_cap, k, E, tiles, static_cast<uint8_t*>(codes), static_cast<uint8_t*>(scales));
+  return launch_kernel(to4_kernel<RAGGED, GATHER>, dim3(grid_for(tiles, k, num_cus, kToGroups)), dim3(kThreads),
+                       stream, in, offs, rows_cap, k, E, tiles, static_cast<uint8_t*>(codes),
+                       static_cast<uint8_t*>(scales));
 }
 
 hipError_t launch_fp4_silu_mul_rows(bool masked, const void* h, const int32_t* groups, int32_t E, int64_t m,
@@ -383,8 +390,8 @@ hipError_t launch_fp4_silu_mul_rows(bool masked, const void* h, const int32_t* g
   const int layout = masked ? MASKED_ROWS : RAGGED;
   const int64_t tiles = fp4_scale_tiles(layout, m, E);
   auto* kernel = masked ? to4_kernel<MASKED_ROWS, SILU> : to4_kernel<RAGGED, SILU>;
-  return launch_kernel(kernel, dim3(grid_for(tiles, width, num_cus)), dim3(kThreads), stream, in, groups, m, width, E,
-                       tiles, static_cast<uint8_t*>(codes), static_cast<uint8_t*>(scales));
+  return launch_kernel(kernel, dim3(grid_for(tiles, width, num_cus, kToGroups)), dim3(kThreads), stream, in, groups, m,
+                       width, E, tiles, static_cast<uint8_t*>(codes), static_cast<uint8_t*>(scales));
 }
 
 hipError_t launch_fp4_dequantize(int layout, const void* codes, const void* scales, const int32_t* groups, int64_t rows,
@@ -394,7 +401,7 @@ hipError_t launch_fp4_dequantize(int layout, const void* codes, const void* scal
   auto* kernel = layout == RAGGED        ? from4_kernel<RAGGED>
                  : layout == MASKED_ROWS ? from4_kernel<MASKED_ROWS>
                                          : from4_kernel<WEIGHTS>;
-  return launch_kernel(kernel, dim3(grid_for(tiles, k, num_cus)), dim3(kThreads), stream,
+  return launch_kernel(kernel, dim3(grid_for(tiles, k, num_cus, kFromGroups)), dim3(kThreads), stream,
                        static_cast<const uint8_t*>(codes), static_cast<const uint8_t*>(scales), groups, rows, k, E,
                        tiles, static_cast<uint16_t*>(out));
 }
@@ -406,7 +413,7 @@ hipError_t launch_fp4_pack_scales(int layout, const void* src, int64_t ld_src, c
   auto* kernel = layout == RAGGED        ? pack4_kernel<RAGGED>
                  : layout == MASKED_ROWS ? pack4_kernel<MASKED_ROWS>
                                          : pack4_kernel<WEIGHTS>;
-  return launch_kernel(kernel, dim3(grid_for(tiles, k, num_cus)), dim3(kThreads), stream,
+  return launch_kernel(kernel, dim3(grid_for(tiles, k, num_cus, kFromGroups)), dim3(kThreads), stream,
                        static_cast<const uint8_t*>(src), ld_src, groups, rows, k, E, tiles,
                        static_cast<uint8_t*>(dst));
 }
