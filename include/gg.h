@@ -4,8 +4,9 @@
  * forms, the masked backward, the SiLU-mul gate/up forward, the grouped
  * bias and its backward, the [E, N, K] weight layout, the steps that
  * produce the grouped layout (offsets, routing, gather, combine), the fp8
- * block-scaled forward, and the steps of a layer that keeps its activations
- * in 8 bits (norm, 8-bit gather, combine gradient, SiLU-mul rows, dW).
+ * block-scaled forward, the steps of a layer that keeps its activations
+ * in 8 bits (norm, 8-bit gather, combine gradient, SiLU-mul rows, dW), 4-bit
+ * rows and weights with their product, and the expert layer for a few tokens.
  *
  * The operation (PyTorch issue #152668, "Easy repro scenario", and its
  * backward): a 2-D activation X[M,K], a packed 3-D weight W[E,K,N] and int32
@@ -24,8 +25,8 @@
  * ------------------------------------
  *  - Tensors are bf16 (uint16 storage), row-major and densely packed, in
  *    device memory the CALLER owns.  The library allocates nothing, frees
- *    nothing, needs no workspace but those that gg_route and gg_rmsnorm_grad
- *    take as an argument, never copies device -> host and never
+ *    nothing, needs no workspace but those that gg_route, gg_rmsnorm_grad and
+ *    the few-token layer take as an argument, never copies device -> host and never
  *    synchronises: it validates the arguments on the host, then enqueues
  *    kernels on `stream` (a hipStream_t; NULL = the default stream) and
  *    returns.  Group sizes stay on the device (TransformerEngine PR #3542,
@@ -749,7 +750,9 @@ gg_status gg_masked_silu_mul_grad(const void* da, const void* h,
  *   y  [m, n] y_dtype; rows past end(E-1) untouched
  *   Products of codes and scales are exact; each 64-deep scaled matrix
  *   instruction's sum is added into an fp32 accumulator.  A scale of 255 gives
- *   NaN in the rows (columns) it belongs to.
+ *   NaN in the rows (columns) it belongs to.  In a last stage that is partly
+ *   filled the packed bytes of blocks past k count as scales of zeros: any
+ *   value but 255 (the calls above write 0).
  * gg_fp4_masked_forward -- the same on the masked layout.
  *
  * Requirements and errors: those of gg_forward, k (I) a multiple of 32,
@@ -827,8 +830,8 @@ gg_status gg_fp4_masked_forward(const void* x, const void* x_scales,
  * gg_fp4_moe_few_tokens takes e2m1 codes [.., k / 2] with packed scales
  * (GG_FP4_WEIGHT), hidden and inter multiples of 32; the activations stay bf16.
  * Sums are fp32 in a fixed order; weights[t, s] silu(.) (.) is kept to 16 bits of
- * mantissa on the way (two bf16 values), out is rounded once.  An infinity or NaN of an expert's
- * weights reaches its own tokens only.
+ * mantissa on the way (two bf16 values), out is rounded once.  An infinity or
+ * NaN of an expert's weights reaches its own tokens only.
  * tokens <= GG_FEW_TOKENS_MAX and tokens * topk <= GG_FEW_SLOTS_MAX
  * (GG_ERR_LIMIT otherwise), and 2 * inter * hidden < 2^30.  No expert that no
  * token chose is read.  Errors otherwise as the GEMM entry points; safe to capture

@@ -14,12 +14,14 @@
 //   SiLU fwd       as forward, 128 activation columns from a gate/up panel
 //   fp8 fwd        expert rows x n        k            X e4m3 (contig)    W[g] [n, k] e4m3 (contig)
 //   fp8 wgrad      k x n                  expert rows  X e4m3 (strided)   dY   (red-strided)
+//   fp4 fwd        expert rows x n        k            X e2m1 (contig)    W[g] [n, k] e2m1 (contig)
 //
 // (The [E, N, K] weight layout of the bf16 passes is these modes with the
 // dimensions exchanged; the host entry points do the mapping.)  Epilogues:
 // fp32 straight from the accumulators, or through LDS for bf16, for fp32
 // wgrad on short experts (fp8 wgrad: on all), for alpha * P + beta * C, for the grouped bias
-// s[i] * bias[g], and for the SiLU-mul activation.
+// s[i] * bias[g], and for the SiLU-mul activation; fp4 through one LDS slot, with
+// the next tile's first loads ahead of the stores (store_tile_early).
 //
 // "red-contig" means the reduction index is the contiguous one in memory;
 // "red-strided" means the tile's row index is.
@@ -27,7 +29,7 @@
 // Data path (no register staging but for the fp8 wgrad's A, see
 // mainloop_x8): every operand tile goes from global memory straight into LDS with buffer loads in LDS mode (16 bytes per lane,
 // 1 KB per wave instruction), one 64-byte-deep reduction stage at a time
-// (32 bf16 or 64 e4m3 values), through a ring of 4 LDS slots, each load
+// (32 bf16, 64 e4m3 or 128 e2m1 values), through a ring of 4 LDS slots, each load
 // issued 3 to 6 ping-pong steps before its first reader.  In the row passes the A
 // operand is staged two stages at a time instead, so that its loads read
 // whole cache lines (the pair layout, stated with dma_pair).  Each operand
@@ -68,7 +70,12 @@
 // the other reads its next fragments from LDS and issues its share of the
 // global->LDS loads, so a load that cannot issue yet or an LDS read in flight
 // holds up only the wave that is not computing.  The fp8 forward runs the
-// same schedule with v_mfma_scale_f32_32x32x64_f8f6f4 (mainloop8_pp).
+// same schedule with v_mfma_scale_f32_32x32x64_f8f6f4 (mainloop8_pp), and so does the
+// fp4 forward, whose stage is two of those instructions deep: a stage costs 1040
+// clocks, of which the matrix cores take 1024, and a tile's first
+// loads, waits and stores 11000 more (128 experts of some 512 rows, k 2048, n 1536:
+// 157 us; 32 of some 2048, k 6144, n 4096: 861 us, 3.8 PFLOP/s at the 1.4 GHz that
+// the power leaves).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -1658,7 +1665,6 @@ __device__ __forceinline__ void store_tile_x8(uint8_t* cbase, uint32_t ldc_bytes
 template <int TMA, bool OUT_F32>
 constexpr int stores_early() { return OUT_F32 ? TMA * TN * 4 : TMA * 4; }
 
-//
 // NT: non-temporal stores where rows begin on cache lines (store_tile_x8's
 // rule): 32 experts of 2048 rows, n 2048, bf16: k 512 99.0 -> 89.9 us, k 2048
 // 189 -> 172; 512 rows each, whose output the caches hold, within 6 % either way.
@@ -2102,7 +2108,8 @@ __global__ __launch_bounds__(NT, 1) void grouped_gemm_kernel(Params p) {
   // k-blocks of scales, fp4: two stage pairs of them (and the scan in them,
   // which is done before they arrive).
   __shared__ __attribute__((aligned(16))) uint8_t smem[NSTAGE * STAGE_BYTES];
-  __shared__ __attribute__((aligned(16))) uint8_t s_sc[is_fp4(MODE) ? 2 * kScaleSlot4 : is_fp8(MODE) ? 2 * kScaleSlot : 16];
+  constexpr int kScaleBytes = is_fp4(MODE) ? 2 * kScaleSlot4 : is_fp8(MODE) ? 2 * kScaleSlot : 16;
+  __shared__ __attribute__((aligned(16))) uint8_t s_sc[kScaleBytes];
   __shared__ int32_t s_end[GG_MAX_GROUPS_DEV];
   __shared__ int32_t s_pref[GG_MAX_GROUPS_DEV + 1];
   __shared__ HalfCount<MODE> s_half[GG_MAX_GROUPS_DEV + 1];
