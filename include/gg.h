@@ -821,7 +821,7 @@ gg_status gg_fp4_masked_forward(const void* x, const void* x_scales,
  *   weights  fp32 [tokens, topk], or NULL for 1
  *   w13      [E, 2 inter, hidden]    the rows of W1 (gate), then of W3 (up)
  *   w2       [E, hidden, inter]
- *   out      [tokens, hidden]        out_dtype
+ *   out      [tokens, hidden]        out_dtype; may be x itself (bf16)
  *   workspace  gg_moe_few_tokens_workspace_bytes(tokens, topk, inter,
  *            num_groups) bytes of device memory, 16-byte aligned, the caller's;
  *            its contents on entry do not matter.  Calls that may overlap (two

@@ -217,3 +217,47 @@ def test_workspace_stream_graph(four, tokens):
         torch.cuda.synchronize()
         assert torch.equal(out, want[i])
         assert torch.equal(layer(*sets[1]), want[1])
+
+
+@pytest.mark.parametrize("four", [False, True])
+def test_two_at_once(four):
+    """Two captured calls with a workspace each, replayed at the same time on two
+    streams; with one workspace, one after the other; out in x's place."""
+    dev = device()
+    layer = Layer(four, 24, 1056, 288, 8)
+    sets = [tuple(t.cuda() for t in inputs(40 + s, tokens, 4, 24, 1056)) for s, tokens in enumerate((7, 50))]
+    want = [layer(*s).clone() for s in sets]
+    say("few tokens: two at once", four)
+    shared = torch.empty(gg.moe_few_tokens_workspace_bytes(50, 4, 288, 24), dtype=U8, device=dev)
+    streams = [torch.cuda.Stream() for _ in sets]
+    torch.cuda.synchronize()
+
+    def capture(spaces):
+        graphs, outs = [], []
+        for s, ws in zip(sets, spaces):
+            outs.append(torch.empty_like(s[0]))
+            graphs.append(torch.cuda.CUDAGraph())
+            with torch.cuda.graph(graphs[-1]):
+                layer(*s, out=outs[-1], workspace=ws)
+        return graphs, outs
+    own = [torch.empty_like(shared) for _ in sets]
+    graphs, outs = capture(own)
+    for _ in range(10):
+        for o in outs:
+            o.zero_()
+        torch.cuda.synchronize()
+        for g, stream in zip(graphs, streams):
+            with torch.cuda.stream(stream):
+                g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, w) for o, w in zip(outs, want))
+    graphs, outs = capture([shared, shared])
+    for _ in range(5):
+        for g in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, w) for o, w in zip(outs, want))
+    for (x, ids, weights), w in zip(sets, want):
+        x = x.clone()
+        assert layer(x, ids, weights, out=x) is x
+        assert torch.equal(x, w)
