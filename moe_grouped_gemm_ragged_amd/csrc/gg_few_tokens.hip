@@ -37,9 +37,9 @@
 // waves 77 us where 8 take 69).
 //
 // Reached, one token 13.0 + 6.9 us (75 MB; 4 bits 7.7 + 5.3, 20 MB), 23 tokens
-// 111 + 60 us (921 MB: 5.4 TB/s), 4 tokens of the wide 4-bit layer 102 + 55 us
-// (620 MB: 3.9 TB/s: the conversions and rows' operands of 4-bit steps beside
-// the same latencies).  Between the two kernels lies 1.1 us.
+// 111 + 60 us (921 MB: 5.4 TB/s), 4 tokens of the wide 4-bit layer 98 + 55 us
+// (620 MB: 4.1 TB/s; the conversions hide behind the loads, strips of half the
+// bytes have the same beginnings and ends).  Between the two kernels lies 1.1 us.
 //
 // Which experts are reached, and by whom, a workgroup's first wave finds from
 // the expert ids; the first workgroup of each expert leaves it in the workspace
@@ -218,7 +218,8 @@ __device__ __forceinline__ int strip_place(int strip, int i) {
 }
 
 // Workgroup b of n runs on XCD b mod 8: neighbouring strips, which share cache
-// lines of scales, to one XCD, 4 in a row.
+// lines of scales, to one XCD, 4 in a row (4 tokens of the wide 4-bit layer: up
+// reads 438 MB in 98 us, with lines shared across XCDs 510 in 102).
 __device__ __forceinline__ int strip_of(int b, int n) {
   return n % 32 != 0 ? b : b / 32 * 32 + b % 8 * 4 + b / 8 % 4;
 }
@@ -489,9 +490,10 @@ __global__ __launch_bounds__(64 * kUpWaves, 4) void few_up_kernel(Few p) {
     for (int m = 0; m < kRowLoads; ++m) xv[m] = get_x(m);
   }
   const int n = (int)strips<FOUR>(p.inter);
-  const int block = p.strips_each == 1 ? strip_of(blockIdx.x, gridDim.x) : (int)blockIdx.x;
+  // strips a grid apart, so that neighbours are read at the same time
+  const int block = strip_of(blockIdx.x, gridDim.x);
   for (int z = 0; z < p.strips_each; ++z) {
-    const int strip = block * p.strips_each + z;
+    const int strip = block + z * (int)gridDim.x;
     if (strip >= n) break;
     const int64_t row0 = strip_first<FOUR>(strip);
     // places 0..7 rows of W1, 8..15 the same rows of W3
@@ -709,12 +711,14 @@ template <bool FOUR>
 hipError_t launch_four(Few p, hipStream_t stream) {
   const int slots = p.tokens * p.topk;
   const int64_t most = slots < p.num_groups ? slots : p.num_groups, n = strips<FOUR>(p.inter);
-  // several strips a workgroup where there are plenty of workgroups
+  // several strips a workgroup where there are plenty of workgroups, and then a
+  // number of these that strip_of takes
   int64_t each = n * most / kUpGroups;
   each = each < 1 ? 1 : each > 8 ? 8 : each;
   p.strips_each = (int32_t)each;
+  const int64_t across = each == 1 ? n : ((n + each - 1) / each + 31) / 32 * 32;
   auto* up = slots <= 64 ? few_up_kernel<FOUR, true> : few_up_kernel<FOUR, false>;
-  const hipError_t e = launch_kernel(up, dim3((unsigned)((n + each - 1) / each), (unsigned)most), dim3(64 * kUpWaves),
+  const hipError_t e = launch_kernel(up, dim3((unsigned)across, (unsigned)most), dim3(64 * kUpWaves),
                                      stream, p);
   if (e != hipSuccess) return e;
   auto* down = p.tokens <= 16 ? few_down_kernel<FOUR, 16, 1> : few_down_kernel<FOUR, kMaxTokens, 1>;
