@@ -74,7 +74,7 @@
 // fp4 forward, whose stage is two of those instructions deep: a stage costs 1040
 // clocks, of which the matrix cores take 1024, and a tile's first
 // loads, waits and stores 11000 more (128 experts of some 512 rows, k 2048, n 1536:
-// 157 us; 32 of some 2048, k 6144, n 4096: 861 us, 3.8 PFLOP/s at the 1.4 GHz that
+// 150 us; 32 of some 2048, k 6144, n 4096: 805 us, 4.1 PFLOP/s at the 1.5 GHz that
 // the power leaves).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -2023,14 +2023,14 @@ __device__ __forceinline__ int find_group(const int32_t* pref, int E, int t) {
 
 // The same by the whole wave at once (fp4): two looks, at every 64th part's
 // first entry and within the part, instead of one for each halving.
-template <typename T>
-__device__ __forceinline__ int find_group_wave(const T* pref, int E, int t, int lane) {
+template <typename F>
+__device__ __forceinline__ int find_group_wave(const F& pref, int E, int t, int lane) {
   const int part = (E + 63) >> 6;
   const int i = lane * part;
-  const int at = (__popcll(__ballot(i < E && (int)pref[i < E ? i : 0] <= t)) - 1) * part;
+  const int at = (__popcll(__ballot(i < E && pref(i < E ? i : 0) <= t)) - 1) * part;
   const int k = at + lane;
   const bool in = lane < part && k < E;
-  return at + __popcll(__ballot(in && (int)pref[in ? k : 0] <= t)) - 1;
+  return at + __popcll(__ballot(in && pref(in ? k : 0) <= t)) - 1;
 }
 
 // ---- tile order -------------------------------------------------------------------
@@ -2163,15 +2163,13 @@ __global__ __launch_bounds__(NT, 1) void grouped_gemm_kernel(Params p) {
   uint8_t* const sa3 = smem + 3 * STAGE_BYTES;
 
   // fp4 tiles are found ahead of their use, with divisions of 32 bits (the grid
-  // then has fewer tiles than that, or the long way is taken).
+  // then has fewer tiles than that, or the long way is taken).  Row tiles count in
+  // the order of rows, half-height ones among the others (see t0 below).
   struct Place {
     int g, ct, rt, row0, rows;
   };
-  auto locate = [&](int64_t t) __attribute__((always_inline)) {
-    const int64_t u = xcd_tile(t, total, false);
-    const bool in_full = u < full_tiles;
-    const int64_t v = in_full ? u : u - full_tiles;
-    const int row_tiles = uniform(in_full ? s_pref[E] : (int)s_half[E]);
+  auto locate = [&](int64_t v) __attribute__((always_inline)) {
+    const int row_tiles = uniform(s_pref[E] + (int)s_half[E]);
     int rt_all, ct;
     if (total < (int64_t(1) << 31)) {
       // strip_order
@@ -2186,9 +2184,9 @@ __global__ __launch_bounds__(NT, 1) void grouped_gemm_kernel(Params p) {
       rt_all = (int)r;
     }
     Place q;
-    q.g = uniform(in_full ? find_group_wave(s_pref, E, rt_all, lane) : find_group_wave(s_half, E, rt_all, lane));
+    q.g = uniform(find_group_wave([&](int i) { return s_pref[i] + (int)s_half[i]; }, E, rt_all, lane));
     const int s = uniform(group_start<MODE>(s_end, q.g)), e = uniform(s_end[q.g]);
-    q.rt = in_full ? rt_all - uniform(s_pref[q.g]) : (e - s - 1) / BM;
+    q.rt = rt_all - uniform(s_pref[q.g]) - uniform((int)s_half[q.g]);
     q.row0 = s + q.rt * BM;
     q.rows = e - q.row0 < BM ? e - q.row0 : BM;
     q.ct = uniform(ct);
@@ -2381,16 +2379,34 @@ __global__ __launch_bounds__(NT, 1) void grouped_gemm_kernel(Params p) {
     }
   };
 
-  if ((int64_t)blockIdx.x >= total) return;
+  if (!is_fp4(MODE) && (int64_t)blockIdx.x >= total) return;
   // Decodes below use an index clamped into the grid, so every Tile is
   // assigned on every path (it stays in scalar registers).
   const int64_t last = total - 1;
+  // fp4: each XCD takes an eighth of the list in one run, so that an expert's
+  // weights go through one L2, where a round's tiles over all XCDs and half-height
+  // tiles in a phase of their own read them again (128 experts of some 512 rows, k
+  // 2048, n 1536: 328 MB read and 150 us against 446 and 158; 32 of some 2048, k 6144,
+  // n 4096: 805 us against 860).  Where all experts of many rows come before all of
+  // few, some XCDs have the long tiles: 64 of 1024 rows, then 256 of 64 345 us
+  // against 327; with the runs cut by the tiles' time 338, but 28 us against 25 for
+  // 64 masked experts of at most 256 rows, k 768, n 2048.
+  [[maybe_unused]] int64_t t0 = blockIdx.x, t1 = total, step4 = gridDim.x;
+  if constexpr (is_fp4(MODE)) {
+    if ((gridDim.x & 7) == 0) {
+      const int x = blockIdx.x & 7;
+      step4 = gridDim.x >> 3;
+      t0 = total * x / 8 + (blockIdx.x >> 3);
+      t1 = total * (x + 1) / 8;
+    }
+  }
   Tile cur;
   [[maybe_unused]] Place next;      // fp4: the tile after cur
   if constexpr (is_fp4(MODE)) {
-    place_tile(locate(blockIdx.x), cur);
+    if (t0 >= t1) return;
+    place_tile(locate(t0), cur);
     issue_prologue(cur);
-    next = locate((int64_t)blockIdx.x + gridDim.x < total ? (int64_t)blockIdx.x + gridDim.x : last);
+    next = locate(t0 + step4 < t1 ? t0 + step4 : t1 - 1);
   } else {
     decode_tile(blockIdx.x, cur);
     issue_prologue(cur);
@@ -2399,7 +2415,8 @@ __global__ __launch_bounds__(NT, 1) void grouped_gemm_kernel(Params p) {
   // The scaled form (alpha != 1 or beta != 0) goes through the LDS epilogue
   // for both output types.
   const bool scaled = p.alpha != 1.0f || p.beta != 0.0f || p.bias != nullptr;
-  for (int64_t t = blockIdx.x; t < total; t += gridDim.x) {
+  for (int64_t t = is_fp4(MODE) ? t0 : blockIdx.x; t < (is_fp4(MODE) ? t1 : total);
+       t += is_fp4(MODE) ? step4 : gridDim.x) {
     floatx16 acc[TM][TN];
 #pragma unroll
     for (int i = 0; i < TM; ++i)
@@ -2447,7 +2464,7 @@ __global__ __launch_bounds__(NT, 1) void grouped_gemm_kernel(Params p) {
                                                     smem + 3 * STAGE_BYTES, cur.A.origin, cur.B.origin, cur.A,
                                                     cur.B, tid, wave, faa, fab, acc, prev_stores);
     }
-    const int64_t tn = t + gridDim.x;
+    const int64_t tn = t + (is_fp4(MODE) ? step4 : gridDim.x);
     if constexpr (is_fp4(MODE)) {
       // every wave is done with the stages, and loads past the end have landed
       // their zeros: slots 0 to 2 take the next tile's first loads, slot 3 the
@@ -2455,7 +2472,7 @@ __global__ __launch_bounds__(NT, 1) void grouped_gemm_kernel(Params p) {
       stage_barrier();
       Tile nxt;
       place_tile(next, nxt);
-      if (tn < total) issue_prologue(nxt);
+      if (tn < t1) issue_prologue(nxt);
       uint8_t* slab = sa3 + wave * (STAGE_BYTES / NWAVE);
       const bool whole_lines = ((cur.ldc_bytes | (uint32_t)reinterpret_cast<uintptr_t>(cur.cbase)) & 127u) == 0u;
 #define GG_STORE_EARLY(H, LINES) \
@@ -2470,8 +2487,8 @@ __global__ __launch_bounds__(NT, 1) void grouped_gemm_kernel(Params p) {
 #undef GG_STORE_EARLY
       cur = nxt;
       // found while the first loads arrive
-      const int64_t tn2 = tn + gridDim.x;
-      next = locate(tn2 < total ? tn2 : last);
+      const int64_t tn2 = tn + step4;
+      next = locate(tn2 < t1 ? tn2 : t1 - 1);
     } else if (OUT_F32 && !STAGED_F32 && !scaled && !is_silu(MODE) && !is_scaled(MODE)) {
       // Every wave is done reading this tile's stages: issue the next
       // tile's prologue loads first, then this tile's stores, so the
