@@ -2134,7 +2134,8 @@ __global__ __launch_bounds__(NT, 1) void grouped_gemm_kernel(Params p) {
   const int col_tiles = (int)((out_cols + kOutCols - 1) / kOutCols);
   // Non-wgrad tiles come in two phases: every full-height row tile, then
   // the half-height last tiles.  Tiles of one phase take the same time, so
-  // the workgroups of an XCD stay in step and share their panels in L2.
+  // the workgroups of an XCD stay in step and share their panels in L2.  (fp4: one
+  // phase, see t0 below.)
   int64_t total;
   int64_t full_tiles = 0;
   int row_tiles_w = 0;
