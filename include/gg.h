@@ -741,7 +741,8 @@ gg_status gg_masked_silu_mul_grad(const void* da, const void* h,
  * gg_fp4_silu_mul_rows, gg_fp4_masked_silu_mul_rows -- 4-bit rows of
  *   a = silu(g) u (in fp32) from gate/up rows h bf16 [m, n], n = 2 I, gate
  *   columns first; I a multiple of 32.
- * gg_fp4_dequantize -- out = code * scale in bf16 [.., k] (exact).  Its uses:
+ * gg_fp4_dequantize -- out = code * scale in bf16 [.., k] (exact; from 2^128
+ *   on, which bf16 does not hold, an infinity).  Its uses:
  *   the operands of a training step's gradients (gg_dgrad_nk, gg_wgrad_nk), and
  *   4-bit weights for the bf16 passes.
  * gg_fp4_forward -- Y[rows of g] = sum_k x sx w[g] sw:
@@ -831,7 +832,9 @@ gg_status gg_fp4_masked_forward(const void* x, const void* x_scales,
  * (GG_FP4_WEIGHT), hidden and inter multiples of 32; the activations stay bf16.
  * Sums are fp32 in a fixed order; weights[t, s] silu(.) (.) is kept to 16 bits of
  * mantissa on the way (two bf16 values), out is rounded once.  An infinity or
- * NaN of an expert's weights reaches its own tokens only.
+ * NaN of an expert's weights reaches its own tokens only, and gives what the
+ * formula does.  4-bit weights count as gg_fp4_dequantize gives them (infinite
+ * from 2^128 on).
  * tokens <= GG_FEW_TOKENS_MAX and tokens * topk <= GG_FEW_SLOTS_MAX
  * (GG_ERR_LIMIT otherwise), and 2 * inter * hidden < 2^30.  No expert that no
  * token chose is read.  Errors otherwise as the GEMM entry points; safe to capture

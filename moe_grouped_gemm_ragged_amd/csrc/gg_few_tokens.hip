@@ -649,7 +649,11 @@ __global__ __launch_bounds__(64 * kDownWaves) void few_down_kernel(Few p) {
   // rows in columns 0..7, lanes 32..63 the second's in 8..15.
   auto add = [&](f32x4f part, uint64_t tokens, int b, int sub) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) part[e] += half_mirror(part[e]);
+    for (int e = 0; e < 4; ++e) {
+      // (an infinite weight times what the bf16 value left is NaN, or of the other sign)
+      const float left = half_mirror(part[e]);
+      part[e] += rows::finite(part[e]) ? left : 0.f;
+    }
     const int i = kQuad * b + (col & 3);
     if ((col & 4) == 0 && i < __popcll(tokens)) {
       uint64_t left = tokens;
