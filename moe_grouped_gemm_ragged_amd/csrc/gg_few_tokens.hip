@@ -70,6 +70,7 @@ constexpr int kUpGroups = 4096;               // up workgroups from which on eac
 constexpr unsigned kDownPairs = 512;          // 4-bit down strips from which on a workgroup takes two
 constexpr int kQuad = 4;                      // tokens of a down product: four columns each
 constexpr uint32_t kOutside = 0x80000000u;    // an offset past every range here
+constexpr float kMaxBf16 = 0x1.fep127f;
 
 typedef __bf16 bf16x8f __attribute__((ext_vector_type(8)));
 typedef float f32x4f __attribute__((ext_vector_type(4)));
@@ -548,7 +549,8 @@ __global__ __launch_bounds__(64 * kUpWaves, 4) void few_up_kernel(Few p) {
           }
           const float a = g * __builtin_amdgcn_rcpf(1.0f + __expf(-g)) * u * s_share[t];
           __bf16* to = reinterpret_cast<__bf16*>(p.act) + (int64_t)(base + t) * 2 * p.inter + c;
-          const __bf16 high = (__bf16)a;
+          // (a finite value above bf16's largest is that and what it left)
+          const __bf16 high = (__bf16)(rows::finite(a) ? __builtin_amdgcn_fmed3f(a, -kMaxBf16, kMaxBf16) : a);
           const float left = a - (float)high;
           to[0] = high;
           // (an infinity or NaN is its own value, with nothing left)

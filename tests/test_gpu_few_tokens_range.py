@@ -1,5 +1,5 @@
-"""The few-token layer at the ends of its number range: infinite weights, and the
-4-bit scales' ends."""
+"""The few-token layer at the ends of its number range: infinite weights, an
+activation next to the largest fp32 value, and the 4-bit scales' ends."""
 import pytest
 import torch
 
@@ -40,6 +40,13 @@ def activations(x, ids, w13, weights):
 
 def random_codes(g, *shape):
     return torch.randint(0, 16, shape, generator=g, dtype=U8)
+
+
+def one_hot(experts, hidden, inter, code=2):
+    """W2 codes with one value a row: out[h] is activation h mod inter times it."""
+    codes = torch.zeros(experts, hidden, inter, dtype=U8)
+    codes[:, torch.arange(hidden), torch.arange(hidden) % inter] = code
+    return codes
 
 
 @pytest.mark.parametrize("four", [False, True])
@@ -83,6 +90,27 @@ def test_infinite_weights(four, dtype, tokens):
     same = (w2.value == clean.value).all(-1)                # [E, hidden]: rows that were not changed
     same = same[ids.long()].all(1)
     assert torch.equal(got[same], before[same]) and bool(same.any())
+
+
+@pytest.mark.parametrize("four", [False, True])
+def test_activation_next_to_fp32_max(four):
+    """An activation of 2^128 - 2^118, which fp32 holds and bf16 rounds to an
+    infinity, reaches out as it is: 2^28 - 2^18 after a weight of 2^-100."""
+    device()
+    hidden, inter = 64, 32
+    codes = torch.zeros(1, 2 * inter, hidden, dtype=U8)
+    codes[:, :, 0] = 2
+    codes[:, inter:, 1] = 2
+    w13 = Weights(four, codes, torch.full((1, 2 * inter, hidden // 32), 127 + 32, dtype=U8))
+    w2 = Weights(four, one_hot(1, hidden, inter), torch.full((1, hidden, inter // 32), 27, dtype=U8))
+    x = torch.zeros(2, hidden, dtype=BF)
+    x[:, 0] = 2.0 ** 32
+    x[0, 1] = -(2.0 ** 22)
+    x[1, 1] = -(2.0 ** 31)              # (an ordinary one: 2^127)
+    ids = torch.zeros(2, 1, dtype=I32)
+    say("few tokens: next to fp32's largest value", four)
+    got = layer(four, x, ids, w13, w2, out_dtype=F32).cpu()
+    assert bool((got[0] == 2.0 ** 28 - 2.0 ** 18).all()) and bool((got[1] == 2.0 ** 27).all())
 
 
 def test_scales_at_their_ends():
