@@ -567,6 +567,14 @@ __device__ __forceinline__ float half_mirror(float v) {
                             __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0x141, 0xf, 0xf, true));
 }
 
+// Between one lane's access to LDS and another's of the same wave: conditions that
+// exclude each other in every lane may otherwise become one instruction, whose
+// lanes would all read what was there before.
+__device__ __forceinline__ void lanes_in_order() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
 // TOKENS: at most.  SUB: strips of a workgroup, side by side in their span (4
 // bits): a step's four loads of rows then serve two of weights.  With both and
 // their scales a strip's step costs the address unit 64 clocks instead of 96.  Where
@@ -657,13 +665,15 @@ __global__ __launch_bounds__(64 * kDownWaves) void few_down_kernel(Few p) {
       part[e] += rows::finite(part[e]) ? left : 0.f;
     }
     const int i = kQuad * b + (col & 3);
-    if ((col & 4) == 0 && i < __popcll(tokens)) {
-      uint64_t left = tokens;
-      for (int z = 0; z < i; ++z) left &= left - 1ull;
-      f32x4f* to = reinterpret_cast<f32x4f*>(&s_out[wave][sub * TOKENS + __ffsll((unsigned long long)left) - 1][4 * (q & 1)]);
-      if (q < 2 && !second) *to = *to + part;
-      if (q >= 2 && second) *to = *to + part;
-    }
+    const bool has = (col & 4) == 0 && i < __popcll(tokens);
+    uint64_t left = tokens;
+    for (int z = 0; z < (has ? i : 0); ++z) left &= left - 1ull;
+    f32x4f* to = reinterpret_cast<f32x4f*>(
+        &s_out[wave][sub * TOKENS + (has ? __ffsll((unsigned long long)left) - 1 : 0)][4 * (q & 1)]);
+    lanes_in_order();
+    if (has && q < 2 && !second) *to = *to + part;
+    lanes_in_order();
+    if (has && q >= 2 && second) *to = *to + part;
   };
   f32x4f part[SUB];
 #pragma unroll
