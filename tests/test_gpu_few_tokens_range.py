@@ -1,10 +1,11 @@
-"""The few-token layer at the ends of its number range: infinite weights, an
-activation next to the largest fp32 value, and the 4-bit scales' ends."""
+"""The few-token layer at the ends of its number range: infinite weights, the
+activation's 16 bits of mantissa on its way between the two kernels, one next to
+the largest fp32 value, and the 4-bit scales' ends."""
 import pytest
 import torch
 
 import fp4_ref
-from layer_ref import TINY, U32
+from layer_ref import TINY, U32, close
 from moe_grouped_gemm_ragged_amd import binding as gg
 from gpu_util import device, say
 
@@ -90,6 +91,33 @@ def test_infinite_weights(four, dtype, tokens):
     same = (w2.value == clean.value).all(-1)                # [E, hidden]: rows that were not changed
     same = same[ids.long()].all(1)
     assert torch.equal(got[same], before[same]) and bool(same.any())
+
+
+@pytest.mark.parametrize("four", [False, True])
+@pytest.mark.parametrize("tokens", [3, 20, 64])
+def test_activation_keeps_16_bits(four, tokens):
+    """x and W13 are whole multiples of 2^-4 or 1, so gate and up are exact in
+    fp32 (multiples of 2^-5 below 2^9).  Each row of W2 has a single 1, so out is
+    the sum of two activations: the bound is 2^-17 of each for its two bf16
+    values (half a step of the second, which is at most half a step of the
+    first), and the fp32 roundings."""
+    device()
+    g = torch.Generator().manual_seed(100 + tokens)
+    experts, hidden, inter, topk = 5, 128, 96, 2
+    w13 = Weights(four, random_codes(g, experts, 2 * inter, hidden), torch.full((experts, 2 * inter, hidden // 32), 123, dtype=U8))
+    w2 = Weights(four, one_hot(experts, hidden, inter), torch.full((experts, hidden, inter // 32), 127, dtype=U8))
+    x = torch.randint(-3, 4, (tokens, hidden), generator=g).to(BF)
+    ids = torch.rand(tokens, experts, generator=g).topk(topk, dim=1).indices.to(I32)
+    weights = torch.rand(tokens, topk, generator=g)
+    a, gate = activations(x, ids, w13, weights)
+    column = torch.arange(hidden) % inter
+    want = a.sum(1)[:, column]
+    # layer_ref.silu_mul's slack, the share's product, the additions over slots, halves and waves
+    slack = a.abs() * (2.0 ** -17 + (2 * gate.abs() + 16 + 2 + 16) * U32) + TINY * (1 + a.abs())
+    say("few tokens: activation", four, tokens)
+    got = layer(four, x, ids, w13, w2, weights, out_dtype=F32)
+    slack = slack.sum(1)[:, column]
+    close(got, want, slack + U32 * (want.abs() + slack), "activation")
 
 
 @pytest.mark.parametrize("four", [False, True])
