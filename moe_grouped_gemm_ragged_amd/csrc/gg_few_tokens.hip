@@ -66,7 +66,8 @@ constexpr int kStrip = 8;                     // weight rows of a strip
 constexpr int kUpWaves = 4, kDownWaves = 8;
 constexpr int kPitch = 2 * kStrip + 1;        // floats between a token's sums in LDS
 constexpr int kRowBytes = 30 << 10;           // x rows of an up workgroup's tokens in LDS, where they fit
-constexpr int kUpGroups = 4096;               // up workgroups from which on each takes several strips
+constexpr int kUpGroups = 4096;               // up workgroups for each strip that one takes,
+constexpr int kUpStrips = 4;                  //   and the most strips (measured beside launch_four)
 constexpr unsigned kDownPairs = 512;          // 4-bit down strips from which on a workgroup takes two
 constexpr int kQuad = 4;                      // tokens of a down product: four columns each
 constexpr uint32_t kOutside = 0x80000000u;    // an offset past every range here
@@ -220,9 +221,10 @@ __device__ __forceinline__ int strip_place(int strip, int i) {
 
 // Workgroup b of n runs on XCD b mod 8: neighbouring strips, which share cache
 // lines of scales, to one XCD, 4 in a row (4 tokens of the wide 4-bit layer: up
-// reads 438 MB in 98 us, with lines shared across XCDs 510 in 102).
+// reads 438 MB in 98 us, with lines shared across XCDs 510 in 102).  What is left
+// of n after whole 32s as it comes.
 __device__ __forceinline__ int strip_of(int b, int n) {
-  return n % 32 != 0 ? b : b / 32 * 32 + b % 8 * 4 + b / 8 % 4;
+  return b >= n / 32 * 32 ? b : b / 32 * 32 + b % 8 * 4 + b / 8 % 4;
 }
 
 struct Few {
@@ -727,12 +729,21 @@ template <bool FOUR>
 hipError_t launch_four(Few p, hipStream_t stream) {
   const int slots = p.tokens * p.topk;
   const int64_t most = slots < p.num_groups ? slots : p.num_groups, n = strips<FOUR>(p.inter);
-  // several strips a workgroup where there are plenty of workgroups, and then a
-  // number of these that strip_of takes
-  int64_t each = n * most / kUpGroups;
-  each = each < 1 ? 1 : each > 8 ? 8 : each;
+  // Several strips a workgroup where there are plenty of workgroups.  The layer in us,
+  // by strips a workgroup (tokens of 8 slots, experts, hidden x inter; * the rule's):
+  //                                 1     2     3     4     6     8
+  //   bf16 23, 128, 2048 x  704   163   159*  162   165   165   174
+  //        23, 128, 2048 x  800   180   178   181*  183   187   194
+  //        64, 512,  512 x  256   128   106   102    99*   95   102
+  //        32, 256, 2048 x 1024   365   348   353   357*  363   368
+  //   4 b   4,  64, 7168 x 2048   162   155*  153   156   163   162
+  //        23, 128, 2048 x  768   106    87    82*   82    82    86
+  //        64, 512,  512 x  256   104    78    71    67*   64    66
+  //        32, 128, 7168 x 2048   741   712   699   715*  715   734
+  const int64_t full = n * most / kUpGroups;
+  const int64_t each = full < 1 ? 1 : full > kUpStrips ? kUpStrips : full;
   p.strips_each = (int32_t)each;
-  const int64_t across = each == 1 ? n : ((n + each - 1) / each + 31) / 32 * 32;
+  const int64_t across = (n + each - 1) / each;
   auto* up = slots <= 64 ? few_up_kernel<FOUR, true> : few_up_kernel<FOUR, false>;
   const hipError_t e = launch_kernel(up, dim3((unsigned)across, (unsigned)most), dim3(64 * kUpWaves),
                                      stream, p);

@@ -34,7 +34,7 @@ class Layer:
         c13[:, :inter, 0] = gate
         c2 = codes(experts, hidden, k2)
         # (so many of W2's values that a sum stays below 2^24)
-        keep = 3000.0 / (topk * inter)
+        keep = 24000.0 / (topk * inter * max(hidden, 64) ** 0.5)
         if keep < 1:
             c2[torch.rand(c2.shape, generator=g, device=dev) >= keep] = 0
         grid = torch.cat([fp4_ref.GRID, -fp4_ref.GRID]).to(dev).to(BF)

@@ -25,3 +25,54 @@ def test_every_product_counts_once(four, tokens, topk, experts, hidden, inter):
     assert bool((want != 0).any())
     for _ in range(3):
         assert torch.equal(layer(x, ids, weights, out_dtype=torch.float32).double(), want)
+
+
+def up_launch(four, slots, experts, inter):
+    """Workgroups of an expert in the up kernel, the strips of each, and all strips."""
+    n = -(-inter // 128) * 16 if four else -(-inter // 8)
+    each = min(max(n * min(slots, experts) // 4096, 1), 4)
+    return -(-n // each), each, n
+
+
+def crowded(seed, tokens, topk, experts, crowd):
+    """Each token's distinct experts; expert i is one of the first crowd[i] tokens' for i < len(crowd)."""
+    ids = exact.some_experts(seed, tokens, topk, experts - len(crowd)) + len(crowd)
+    for i, c in enumerate(crowd):
+        ids[:c, i] = i
+    return ids
+
+
+# tokens, topk, experts, hidden, inter, tokens of the first experts: several strips a workgroup, an even
+# and an odd share, with 1, 2 and 4 blocks of 16 tokens, x in LDS or not, at most 64 slots and more
+STRIPS = [
+    (8, 8, 64, 64, 1024, ()), (8, 8, 64, 96, 1088, (8,)), (23, 8, 128, 64, 768, (20, 16, 1)), (23, 8, 128, 64, 704, (23,)),
+    (23, 8, 128, 88, 800, (9,)),
+    (64, 8, 128, 64, 768, (64, 33, 17, 16, 32)), (64, 8, 100, 32, 1344, (40, 16)), (16, 8, 64, 1056, 1024, (16, 15, 13)),
+    (64, 8, 512, 64, 256, (50, 16)), (64, 8, 256, 32, 544, (64, 18)),
+]
+
+
+@pytest.mark.parametrize("four", [False, True])
+@pytest.mark.parametrize("tokens,topk,experts,hidden,inter,crowd", STRIPS)
+def test_several_strips_a_workgroup(four, tokens, topk, experts, hidden, inter, crowd):
+    device()
+    across, each, n = up_launch(four, tokens * topk, experts, inter)
+    assert each > 1 and across < n
+    if four:
+        hidden = -(-hidden // 32) * 32
+    layer = exact.Layer(four, experts, hidden, inter, topk, seed=inter)
+    x, ids, weights = exact.inputs(inter, tokens, hidden, crowded(tokens, tokens, topk, experts, crowd))
+    assert all(int((ids == i).sum()) == c for i, c in enumerate(crowd))
+    say("few tokens: several strips", four, tokens, experts, hidden, inter, (across, each, n))
+    want = layer.want(x, ids, weights)
+    for _ in range(3):
+        assert torch.equal(layer(x, ids, weights, out_dtype=torch.float32).double(), want)
+
+
+def test_strips_cover_the_rule():
+    """The cases above take 2, 3 and 4 strips, whole shares and a last one that is
+    smaller, workgroups in and past whole 32s."""
+    seen = [up_launch(four, c[0] * c[1], c[2], c[4]) for c in STRIPS for four in (False, True)]
+    assert {s[1] for s in seen} == {2, 3, 4}
+    assert any(across * each > n for across, each, n in seen) and any(across * each == n for across, each, n in seen)
+    assert any(across < 32 for across, _, _ in seen) and any(across > 32 and across % 32 for across, _, _ in seen)
