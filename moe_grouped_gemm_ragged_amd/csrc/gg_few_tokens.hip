@@ -68,7 +68,7 @@ constexpr int kPitch = 2 * kStrip + 1;        // floats between a token's sums i
 constexpr int kRowBytes = 30 << 10;           // x rows of an up workgroup's tokens in LDS, where they fit
 constexpr int kUpGroups = 4096;               // up workgroups for each strip that one takes,
 constexpr int kUpStrips = 4;                  //   and the most strips (measured beside launch_four)
-constexpr unsigned kDownPairs = 512;          // 4-bit down strips from which on a workgroup takes two
+constexpr unsigned kDownAlone = 256;          // 4-bit down strips up to which each has a workgroup of its own
 constexpr int kQuad = 4;                      // tokens of a down product: four columns each
 constexpr uint32_t kOutside = 0x80000000u;    // an offset past every range here
 constexpr float kMaxBf16 = 0x1.fep127f;
@@ -579,10 +579,16 @@ __device__ __forceinline__ void lanes_in_order() {
 
 // TOKENS: at most.  SUB: strips of a workgroup, side by side in their span (4
 // bits): a step's four loads of rows then serve two of weights.  With both and
-// their scales a strip's step costs the address unit 64 clocks instead of 96.  Where
-// every compute unit keeps a workgroup: some 25 experts of 7168 x 2048 69 -> 55 us, 8
-// of them 23.5 -> 21.6, some 40 of 4096 x 1536 49 -> 37; 64 workgroups of 128 strips 4.6 ->
-// 5.5, so fewer than kDownPairs strips keep one each.
+// their scales a strip's step costs the address unit 64 clocks instead of 96: some 25
+// experts of 7168 x 2048 69 -> 55 us, 8 of them 23.5 -> 21.6.  Up to one strip for each
+// compute unit they stay alone.  The layer in us, one strip a workgroup and two:
+//   strips  1 token, I 768   4 tokens, I 2048   23 tokens, I 768   64 tokens, I 768
+//     128     11.6   12.6       51.6   57.9        70.6   81.0       136    157
+//     256     12.6   13.6       59.8   66.1        81.9   92.0       153    174
+//     368     14.9   14.5       86.3   77.6       127.0  108.8       244    202
+//     512     16.7   16.3      100.2   91.9       149.2  130.8       283    242
+//     640     20.6   22.1      131.8  132.1       198.7  195.3       382    372
+//     896     24.7   24.7      167.8  153.9       262.2  233.8       509    440
 template <bool FOUR, int TOKENS, int SUB>
 __global__ __launch_bounds__(64 * kDownWaves) void few_down_kernel(Few p) {
   static_assert(SUB == 1 || FOUR, "bf16 strips do not share a span");
@@ -751,7 +757,7 @@ hipError_t launch_four(Few p, hipStream_t stream) {
   auto* down = p.tokens <= 16 ? few_down_kernel<FOUR, 16, 1> : few_down_kernel<FOUR, kMaxTokens, 1>;
   unsigned groups = (unsigned)strips<FOUR>(p.hidden);
   if constexpr (FOUR) {
-    if (groups >= kDownPairs) {
+    if (groups > kDownAlone) {
       down = p.tokens <= 16 ? few_down_kernel<FOUR, 16, 2> : few_down_kernel<FOUR, kMaxTokens, 2>;
       groups /= 2;
     }

@@ -76,3 +76,16 @@ def test_strips_cover_the_rule():
     assert {s[1] for s in seen} == {2, 3, 4}
     assert any(across * each > n for across, each, n in seen) and any(across * each == n for across, each, n in seen)
     assert any(across < 32 for across, _, _ in seen) and any(across > 32 and across % 32 for across, _, _ in seen)
+
+
+@pytest.mark.parametrize("four", [False, True])
+@pytest.mark.parametrize("tokens,topk,experts", [(1, 8, 16), (19, 3, 10), (64, 2, 7)])
+@pytest.mark.parametrize("hidden", [2016, 2048, 2080, 2880, 4096])
+def test_widths_around_a_strip_for_each_compute_unit(four, tokens, topk, experts, hidden):
+    """4 bits: 256 strips of the down product and the next more, where workgroups
+    begin to take two; a last span that is not full."""
+    device()
+    layer = exact.Layer(four, experts, hidden, 288, topk, seed=hidden)
+    x, ids, weights = exact.inputs(hidden, tokens, hidden, exact.some_experts(tokens, tokens, topk, experts, 0.1))
+    say("few tokens: widths", four, tokens, experts, hidden)
+    assert torch.equal(layer(x, ids, weights, out_dtype=torch.float32).double(), layer.want(x, ids, weights))
