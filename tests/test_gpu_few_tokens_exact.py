@@ -89,3 +89,41 @@ def test_widths_around_a_strip_for_each_compute_unit(four, tokens, topk, experts
     x, ids, weights = exact.inputs(hidden, tokens, hidden, exact.some_experts(tokens, tokens, topk, experts, 0.1))
     say("few tokens: widths", four, tokens, experts, hidden)
     assert torch.equal(layer(x, ids, weights, out_dtype=torch.float32).double(), layer.want(x, ids, weights))
+
+
+def reaching(seed, tokens, topk, reached, experts):
+    """Ids that reach so many experts: each once, the other slots to the first
+    of them, more than four tokens each where there are slots enough."""
+    g = torch.Generator().manual_seed(seed)
+    mine = torch.randperm(experts, generator=g)[:reached]
+    rest = tokens * topk - reached
+    crowd = max(1, min(reached, rest // 6))
+    slots = torch.cat([mine, mine[torch.arange(rest) % crowd]])
+    return slots[torch.randperm(slots.numel(), generator=g)].reshape(tokens, topk)
+
+
+# tokens, topk, experts, reached, hidden, inter.  Down: up to 64 reached experts one list, then each wave its
+# own; from 256 on whole experts a wave, below equal runs of steps that begin inside an expert.  An expert has
+# inter / 128 steps in bf16 and inter / 256 in 4 bits, rounded up
+REACHED = [
+    (64, 8, 70, 64, 64, 544), (64, 8, 70, 65, 64, 544), (64, 8, 128, 100, 96, 288), (13, 8, 300, 97, 64, 800),
+    (64, 8, 300, 255, 64, 544), (32, 8, 300, 256, 64, 288), (64, 8, 300, 256, 64, 544), (64, 8, 300, 300, 32, 800),
+    (64, 8, 512, 512, 64, 288), (1, 65, 65, 65, 64, 544), (1, 512, 512, 400, 32, 288), (64, 8, 2048, 450, 32, 288),
+    (64, 8, 100, 100, 2080, 288), (64, 8, 280, 257, 2080, 288),
+]
+
+
+@pytest.mark.parametrize("four", [False, True])
+@pytest.mark.parametrize("tokens,topk,experts,reached,hidden,inter", REACHED)
+def test_many_reached_experts(four, tokens, topk, experts, reached, hidden, inter):
+    device()
+    slots = reaching(reached, tokens, topk, reached, experts)
+    assert len(set(slots.reshape(-1).tolist())) == reached
+    if tokens * topk - reached > 60 and tokens > 8:
+        assert max((slots == e).any(-1).sum().item() for e in range(experts)) > 4
+    layer = exact.Layer(four, experts, hidden, inter, topk, seed=reached)
+    x, ids, weights = exact.inputs(reached, tokens, hidden, slots)
+    say("few tokens: reached experts", four, tokens, experts, reached, hidden, inter)
+    want = layer.want(x, ids, weights)
+    for _ in range(3):
+        assert torch.equal(layer(x, ids, weights, out_dtype=torch.float32).double(), want)
