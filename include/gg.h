@@ -739,8 +739,9 @@ gg_status gg_masked_silu_mul_grad(const void* da, const void* h,
  *   below the last end offset; zero codes and the scale 1 for a padding row.
  *   src [tokens, k] bf16; row_slot and offs as gg_route wrote them.
  * gg_fp4_silu_mul_rows, gg_fp4_masked_silu_mul_rows -- 4-bit rows of
- *   a = silu(g) u (in fp32) from gate/up rows h bf16 [m, n], n = 2 I, gate
- *   columns first; I a multiple of 32.
+ *   a = silu(g) u (in fp32; 1 / (1 + exp(-g)) counts as 0 below 2^-126, as in
+ *   every SiLU here) from gate/up rows h bf16 [m, n], n = 2 I, gate columns
+ *   first; I a multiple of 32.
  * gg_fp4_dequantize -- out = code * scale in bf16 [.., k] (exact; from 2^128
  *   on, which bf16 does not hold, an infinity).  Its uses:
  *   the operands of a training step's gradients (gg_dgrad_nk, gg_wgrad_nk), and
