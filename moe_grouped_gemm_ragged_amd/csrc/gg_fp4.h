@@ -24,16 +24,15 @@
 
 #include "gg_internal.h"
 #include "gg_rows.h"
+#include "gg_tiles.h"
 
 namespace gg {
 namespace fp4 {
 
 constexpr int kBlock4 = 32;        // values per scale
 constexpr int kStage4 = 128;       // values per stage
-constexpr int kTileRows = 256;     // rows per packed tile
+using tiles::kTileRows;
 constexpr int kStageBytes = 1024;  // packed scales of a tile and stage
-
-enum Layout { RAGGED = 0, MASKED_ROWS = 1, WEIGHTS = 2 };
 
 __host__ __device__ inline int64_t stages4(int64_t k) { return (k + kStage4 - 1) / kStage4; }
 

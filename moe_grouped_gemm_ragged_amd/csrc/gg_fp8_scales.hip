@@ -18,39 +18,16 @@
 #include <stdint.h>
 
 #include "gg_internal.h"
+#include "gg_tiles.h"
 
 namespace gg {
 namespace {
 
-constexpr int kRows = 256;     // rows per packed tile
-constexpr int kThreads = 256;
+using namespace tiles;
+
+constexpr int kRows = kTileRows;
 constexpr int kChunk = 32;     // k-blocks of a tile staged in LDS at a time
 constexpr int kPitch = kRows + 4;   // LDS bytes per staged k-block (padded: the 32 k-blocks of one row fall in 32 banks)
-
-// Block-wide scan of one non-negative int per thread (sum, or max): a
-// shuffle scan within each wave, then the totals of the earlier waves.
-// Returns the inclusive value; *excl gets the exclusive one (0 for thread 0).
-template <bool MAX>
-__device__ __forceinline__ int block_scan(int v, int* wave_tot, int tid, int* excl) {
-  const int lane = tid & 63, w = tid >> 6;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int o = __shfl_up(v, (unsigned)d, 64);
-    if (lane >= d) v = MAX ? (v > o ? v : o) : v + o;
-  }
-  int prev = __shfl_up(v, 1u, 64);
-  if (lane == 0) prev = 0;
-  if (lane == 63) wave_tot[w] = v;
-  __syncthreads();
-  int before = 0;
-  for (int q = 0; q < w; ++q) {
-    const int t = wave_tot[q];
-    before = MAX ? (before > t ? before : t) : before + t;
-  }
-  __syncthreads();
-  *excl = MAX ? (prev > before ? prev : before) : prev + before;
-  return MAX ? (v > before ? v : before) : v + before;
-}
 
 // E8M0 byte of one scale, and whether the scale is UE8M0: an fp32 with
 // sign and mantissa bits clear (+0.0 or a positive power of two; +0.0 maps
@@ -68,9 +45,7 @@ __device__ __forceinline__ uint32_t e8m0(const void* src, int64_t idx, int& bad)
   }
 }
 
-// LAYOUT 0: ragged activations (groups = end offsets, rows = M);
-// 1: masked activations (groups = masked_m, rows = max_m per expert);
-// 2: weights (rows = N per expert, groups unused).  VEC: fp32 scales read
+// VEC: fp32 scales read
 // four k-blocks per 16-byte load (the row pitch and the k-block count are
 // multiples of 4 and the source is 16-byte aligned).
 typedef uint32_t u32x4s __attribute__((ext_vector_type(4)));
@@ -80,9 +55,7 @@ __global__ __launch_bounds__(kThreads) void pack_scales_kernel(const void* src, 
                                                                int32_t kblocks, int32_t num_groups,
                                                                int64_t tiles, uint8_t* dst,
                                                                int32_t* bad_count) {
-  __shared__ int32_t s_end[GG_MAX_GROUPS_DEV];
-  __shared__ int32_t s_pref[GG_MAX_GROUPS_DEV + 1];
-  __shared__ int32_t s_wave[kThreads / 64];
+  __shared__ std::conditional_t<LAYOUT == RAGGED, Tiles, NoTiles> s_tiles;
   __shared__ uint8_t s_bytes[kChunk * kPitch];
   __shared__ int32_t s_bad;
   const int tid = threadIdx.x;
@@ -90,43 +63,7 @@ __global__ __launch_bounds__(kThreads) void pack_scales_kernel(const void* src, 
   if (tid == 0) s_bad = 0;
   __syncthreads();
   int64_t total = tiles;
-  if constexpr (LAYOUT == 0) {
-    // clamped monotone ends (prefix max of the offsets, capped at rows) and
-    // the prefix of per-expert 256-row tile counts, as the GEMM decodes them
-    const int per = (E + kThreads - 1) / kThreads;
-    const int g0 = tid * per;
-    const int g1 = g0 + per < E ? g0 + per : E;
-    int run = 0;
-    for (int g = g0; g < g1; ++g) {
-      const int o = groups[g];
-      run = o > run ? o : run;
-      s_end[g] = run;
-    }
-    int before;
-    block_scan<true>(run, s_wave, tid, &before);
-    int local = 0;
-    for (int g = g0; g < g1; ++g) {
-      int e = s_end[g] > before ? s_end[g] : before;
-      e = e < rows ? e : (int)rows;
-      s_end[g] = e;
-    }
-    __syncthreads();
-    for (int g = g0; g < g1; ++g) {
-      const int start = g == 0 ? 0 : s_end[g - 1];
-      local += (s_end[g] - start + kRows - 1) / kRows;
-    }
-    int acc;
-    const int incl = block_scan<false>(local, s_wave, tid, &acc);
-    for (int g = g0; g < g1; ++g) {
-      s_pref[g] = acc;
-      const int start = g == 0 ? 0 : s_end[g - 1];
-      acc += (s_end[g] - start + kRows - 1) / kRows;
-    }
-    if (tid == kThreads - 1) s_pref[E] = incl;
-    __syncthreads();
-    total = s_pref[E];
-  }
-  const int64_t tpe = (rows + kRows - 1) / kRows;   // layouts 1, 2: tiles per expert
+  if constexpr (LAYOUT == RAGGED) total = decode_tiles(s_tiles, groups, rows, E, tid);
   int bad = 0;
   // Thread t writes dword d = t mod 64 of k-blocks t / 64, t / 64 + 4, ...:
   // the bytes of tile rows 128 (d / 32) + d mod 32 + 32 b, b = 0..3.  VEC:
@@ -140,30 +77,9 @@ __global__ __launch_bounds__(kThreads) void pack_scales_kernel(const void* src, 
   const int kb0 = tid >> 6;
   for (int64_t T = blockIdx.x; T < total; T += gridDim.x) {
     int64_t first;     // source row of tile row 0
-    int64_t valid;     // rows of the tile that are active
-    if constexpr (LAYOUT == 0) {
-      int lo = 0, hi = E;                 // largest g with s_pref[g] <= T
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (s_pref[mid] <= T) lo = mid; else hi = mid;
-      }
-      const int start = lo == 0 ? 0 : s_end[lo - 1];
-      first = start + (T - s_pref[lo]) * kRows;
-      valid = s_end[lo] - first;
-    } else {
-      const int64_t e = T / tpe;
-      const int64_t r0 = (T - e * tpe) * kRows;
-      first = e * rows + r0;
-      int64_t active = rows;
-      if constexpr (LAYOUT == 1) {
-        int64_t a = groups[e];
-        a = a < 0 ? 0 : a;
-        active = a < rows ? a : rows;
-      }
-      valid = active - r0;
-    }
+    int valid;         // rows of the tile that are active
+    tile_rows<LAYOUT>(s_tiles, groups, rows, E, T, first, valid);
     if constexpr (VEC) {
-      const int nvalid = valid < 0 ? 0 : (valid > kRows ? kRows : (int)valid);
       const int q4 = 4 * (tid & 7);
       const float* srcf = reinterpret_cast<const float*>(src);
       for (int kc = 0; kc < kblocks; kc += kChunk) {
@@ -171,7 +87,7 @@ __global__ __launch_bounds__(kThreads) void pack_scales_kernel(const void* src, 
 #pragma unroll 8
         for (int r = tid >> 3; r < kRows; r += kThreads / 8) {
           u32x4s v = {0u, 0u, 0u, 0u};
-          const bool live = q4 < nk && r < nvalid;
+          const bool live = q4 < nk && r < valid;
           if (live) v = *reinterpret_cast<const u32x4s*>(srcf + (first + r) * ld_src + kc + q4);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -231,7 +147,7 @@ hipError_t launch_layout(bool src_f32, const void* src, int64_t ld_src, const in
 
 int64_t fp8_scale_tiles(int layout, int64_t rows, int32_t num_groups) {
   const int64_t t = (rows + kRows - 1) / kRows;
-  return layout == 0 ? t + num_groups : t * num_groups;
+  return layout == RAGGED ? t + num_groups : t * num_groups;
 }
 
 hipError_t launch_pack_scales(int layout, bool src_f32, const void* src, int64_t ld_src,
@@ -239,12 +155,12 @@ hipError_t launch_pack_scales(int layout, bool src_f32, const void* src, int64_t
                               uint8_t* dst, int32_t* bad, int num_cus, hipStream_t stream) {
   const int64_t tiles = fp8_scale_tiles(layout, rows, num_groups);
   switch (layout) {
-    case 0: return launch_layout<0>(src_f32, src, ld_src, groups, rows, kblocks, num_groups, tiles, dst,
-                                    bad, num_cus, stream);
-    case 1: return launch_layout<1>(src_f32, src, ld_src, groups, rows, kblocks, num_groups, tiles, dst,
-                                    bad, num_cus, stream);
-    default: return launch_layout<2>(src_f32, src, ld_src, groups, rows, kblocks, num_groups, tiles, dst,
-                                     bad, num_cus, stream);
+    case RAGGED: return launch_layout<RAGGED>(src_f32, src, ld_src, groups, rows, kblocks, num_groups, tiles, dst,
+                                              bad, num_cus, stream);
+    case MASKED_ROWS: return launch_layout<MASKED_ROWS>(src_f32, src, ld_src, groups, rows, kblocks, num_groups,
+                                                        tiles, dst, bad, num_cus, stream);
+    default: return launch_layout<WEIGHTS>(src_f32, src, ld_src, groups, rows, kblocks, num_groups, tiles, dst,
+                                           bad, num_cus, stream);
   }
 }
 
