@@ -53,8 +53,9 @@ KERNEL_SRC = os.path.join(ROOT, "moe_grouped_gemm_ragged_amd", "csrc", "gg_kerne
 #     by the factor the same counter reads for `bench.py --copy-calibration`;
 #   clock_GHz: sustained shader clock, GRBM_GUI_ACTIVE / 8 XCDs / kernel time;
 #   mfma_busy: SQ_VALU_MFMA_BUSY_CYCLES / (1024 SIMDs x cycles per XCD).
-# Last dispatch of each run.  Valid only for the kernel source they were
-# taken on (sha256 below); for any other source these fields are null.
+# Last dispatch of each run.  Valid for the kernel source whose sha256 stands
+# below, whose bf16 and fp8 kernels assemble to the same code as the source
+# that the readings were taken on; for any other source these fields are null.
 MEASURED = {
     "kernel_sha256": "9d779d1475dc844ad6d7da2e4abd0d5ae41bce8462eb6c1111c8f1a0dc20b114",
     "glm_up": {"fwd": {"traffic": 23623406989, "clock_GHz": 1.564, "mfma_busy": 0.791},

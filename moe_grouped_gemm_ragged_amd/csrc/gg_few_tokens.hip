@@ -36,10 +36,16 @@
 // waves 120, 15.0 and 11.8 us where 4 take 113, 13.0 and 7.7; down with 16
 // waves 77 us where 8 take 69).
 //
-// Reached, one token 13.0 + 6.9 us (75 MB; 4 bits 7.7 + 5.3, 20 MB), 23 tokens
+// Reached, one token 13.0 + 6.9 us (75 MB, 20.0 in a row of passes, 22.7 with weights
+// that no cache holds; 4 bits 7.7 + 5.3, 20 MB, 11.6 and 13.5), 23 tokens
 // 111 + 60 us (921 MB: 5.4 TB/s), 4 tokens of the wide 4-bit layer 98 + 55 us
 // (620 MB: 4.1 TB/s; the conversions hide behind the loads, strips of half the
 // bytes have the same beginnings and ends).  Between the two kernels lies 1.1 us.
+//
+// An expert of many tokens costs more than its weights: one operand holds 16 of them
+// in the up kernel and 4 in the down kernel, and every strip loads their rows (8
+// experts of 2048 x 768, bf16, 75 MB: 16 tokens each 45 us, 32 88, 33, where the up
+// kernel begins to read its weights twice, 106, and 64 215).
 //
 // Which experts are reached, and by whom, a workgroup's first wave finds from
 // the expert ids; the first workgroup of each expert leaves it in the workspace

@@ -71,11 +71,14 @@
 // global->LDS loads, so a load that cannot issue yet or an LDS read in flight
 // holds up only the wave that is not computing.  The fp8 forward runs the
 // same schedule with v_mfma_scale_f32_32x32x64_f8f6f4 (mainloop8_pp), and so does the
-// fp4 forward, whose stage is two of those instructions deep: a stage costs 1040
-// clocks, of which the matrix cores take 1024, and a tile's first
-// loads, waits and stores 11000 more (128 experts of some 512 rows, k 2048, n 1536:
-// 150 us; 32 of some 2048, k 6144, n 4096: 805 us, 4.1 PFLOP/s at the 1.5 GHz that
-// the power leaves).
+// fp4 forward, whose stage is two of those instructions deep.  32 experts of 2048
+// rows, n 4096, which are 16 tiles a compute unit: k 128 106 us (537 MB of output at a
+// copy's rate), 512 139, 2048 299, 4096 547, 6144 769, so 0.87 to 0.97 us for each
+// further stage of a tile, 4.4 to 4.9 PFLOP/s, and 50 us beside the stages.  With uneven
+// experts k 6144 takes 810 us in a row of passes (by itself, under a trace, 930 in the
+// median and 804 at the least): the matrix cores are busy 65 % of its clocks, at 1.4 to
+// 1.5 GHz, and 2.0 GB are read where 0.64 would do.  128 experts of some 512 rows, k
+// 2048, n 1536: 150 us.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
