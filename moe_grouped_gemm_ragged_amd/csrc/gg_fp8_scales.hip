@@ -64,6 +64,7 @@ __global__ __launch_bounds__(kThreads) void pack_scales_kernel(const void* src, 
   __syncthreads();
   int64_t total = tiles;
   if constexpr (LAYOUT == RAGGED) total = decode_tiles(s_tiles, groups, rows, E, tid);
+  const int64_t tpe = (rows + kRows - 1) / kRows;   // masked, weights: tiles per expert
   int bad = 0;
   // Thread t writes dword d = t mod 64 of k-blocks t / 64, t / 64 + 4, ...:
   // the bytes of tile rows 128 (d / 32) + d mod 32 + 32 b, b = 0..3.  VEC:
@@ -77,9 +78,27 @@ __global__ __launch_bounds__(kThreads) void pack_scales_kernel(const void* src, 
   const int kb0 = tid >> 6;
   for (int64_t T = blockIdx.x; T < total; T += gridDim.x) {
     int64_t first;     // source row of tile row 0
-    int valid;         // rows of the tile that are active
-    tile_rows<LAYOUT>(s_tiles, groups, rows, E, T, first, valid);
+    int64_t valid;     // rows of the tile that are active
+    if constexpr (LAYOUT == RAGGED) {
+      int v;
+      tile_rows<LAYOUT>(s_tiles, groups, rows, E, T, first, v);
+      valid = v;
+    } else {
+      // (tile_rows' arithmetic but for its last clamp, which this kernel makes
+      // where it needs it: 3 % of these layouts' time)
+      const int64_t e = T / tpe;
+      const int64_t r0 = (T - e * tpe) * kRows;
+      first = e * rows + r0;
+      int64_t active = rows;
+      if constexpr (LAYOUT == MASKED_ROWS) {
+        int64_t a = groups[e];
+        a = a < 0 ? 0 : a;
+        active = a < rows ? a : rows;
+      }
+      valid = active - r0;
+    }
     if constexpr (VEC) {
+      const int nvalid = valid < 0 ? 0 : (valid > kRows ? kRows : (int)valid);
       const int q4 = 4 * (tid & 7);
       const float* srcf = reinterpret_cast<const float*>(src);
       for (int kc = 0; kc < kblocks; kc += kChunk) {
@@ -87,7 +106,7 @@ __global__ __launch_bounds__(kThreads) void pack_scales_kernel(const void* src, 
 #pragma unroll 8
         for (int r = tid >> 3; r < kRows; r += kThreads / 8) {
           u32x4s v = {0u, 0u, 0u, 0u};
-          const bool live = q4 < nk && r < valid;
+          const bool live = q4 < nk && r < nvalid;
           if (live) v = *reinterpret_cast<const u32x4s*>(srcf + (first + r) * ld_src + kc + q4);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
