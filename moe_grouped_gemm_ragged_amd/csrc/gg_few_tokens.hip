@@ -575,12 +575,11 @@ __device__ __forceinline__ float half_mirror(float v) {
                             __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0x141, 0xf, 0xf, true));
 }
 
-// Between one lane's access to LDS and another's of the same wave: conditions that
-// exclude each other in every lane may otherwise become one instruction, whose
-// lanes would all read what was there before.
-__device__ __forceinline__ void lanes_in_order() {
-  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-  __builtin_amdgcn_wave_barrier();
+// The value of the lane 40 on (lanes 0..7 of each of the first two rows of 16):
+// columns 8..15 of the row two on.
+__device__ __forceinline__ float second_half(float v) {
+  const uint32_t x = __builtin_bit_cast(uint32_t, rows::row_ror<8>(v));
+  return __builtin_bit_cast(float, (uint32_t)__builtin_amdgcn_permlane32_swap(x, x, false, false)[1]);
 }
 
 // TOKENS: at most.  SUB: strips of a workgroup, side by side in their span (4
@@ -670,24 +669,25 @@ __global__ __launch_bounds__(64 * kDownWaves) void few_down_kernel(Few p) {
   // Adds tokens 4 b .. of an expert's product to the wave's sums.  (Each
   // expert's product is one of its own, so that a weight that is not finite
   // reaches the expert's own tokens only.)  Lanes 0..31 hold the first half's
-  // rows in columns 0..7, lanes 32..63 the second's in 8..15.
+  // rows in columns 0..7, lanes 32..63 the second's in 8..15: one lane adds both
+  // (two lanes in turn, under conditions that exclude each other, may become one
+  // instruction, which would lose one of the two).
   auto add = [&](f32x4f part, uint64_t tokens, int b, int sub) {
+    f32x4f other;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       // (an infinite weight times what the bf16 value left is NaN, or of the other sign)
       const float left = half_mirror(part[e]);
       part[e] += rows::finite(part[e]) ? left : 0.f;
+      other[e] = second_half(part[e]);
     }
     const int i = kQuad * b + (col & 3);
-    const bool has = (col & 4) == 0 && i < __popcll(tokens);
-    uint64_t left = tokens;
-    for (int z = 0; z < (has ? i : 0); ++z) left &= left - 1ull;
-    f32x4f* to = reinterpret_cast<f32x4f*>(
-        &s_out[wave][sub * TOKENS + (has ? __ffsll((unsigned long long)left) - 1 : 0)][4 * (q & 1)]);
-    lanes_in_order();
-    if (has && q < 2 && !second) *to = *to + part;
-    lanes_in_order();
-    if (has && q >= 2 && second) *to = *to + part;
+    if ((col & 4) == 0 && q < 2 && !second && i < __popcll(tokens)) {
+      uint64_t left = tokens;
+      for (int z = 0; z < i; ++z) left &= left - 1ull;
+      f32x4f* to = reinterpret_cast<f32x4f*>(&s_out[wave][sub * TOKENS + __ffsll((unsigned long long)left) - 1][4 * (q & 1)]);
+      *to = *to + part + other;
+    }
   };
   f32x4f part[SUB];
 #pragma unroll
