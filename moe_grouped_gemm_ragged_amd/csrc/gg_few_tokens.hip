@@ -74,7 +74,8 @@ constexpr int kPitch = 2 * kStrip + 1;        // floats between a token's sums i
 constexpr int kRowBytes = 30 << 10;           // x rows of an up workgroup's tokens in LDS, where they fit
 constexpr int kUpGroups = 4096;               // up workgroups for each strip that one takes,
 constexpr int kUpStrips = 4;                  //   and the most strips (measured beside launch_four)
-constexpr unsigned kDownAlone = 256;          // 4-bit down strips up to which each has a workgroup of its own
+constexpr unsigned kDownAlone = 256;          // 4-bit down strips up to which each has a workgroup of its own,
+constexpr int kDownCrowd = 8;                 //   and slots an expert on average from which on it has too
 constexpr int kQuad = 4;                      // tokens of a down product: four columns each
 constexpr uint32_t kOutside = 0x80000000u;    // an offset past every range here
 constexpr float kMaxBf16 = 0x1.fep127f;
@@ -586,10 +587,16 @@ __device__ __forceinline__ float second_half(float v) {
 // bits): a step's four loads of rows then serve two of weights.  With both and
 // their scales a strip's step costs the address unit 64 clocks instead of 96: some 25
 // experts of 7168 x 2048 69 -> 55 us, 8 of them 23.5 -> 21.6.  Up to one strip for each
-// compute unit they stay alone.  The layer in us, one strip a workgroup and two:
+// compute unit they stay alone, and where experts have so many tokens that their
+// rows, not the weights, take the time (I 768, 16 experts, 320 strips: 8 slots an
+// expert 56.2 us alone and 54.2 in pairs, 32 slots 170 and 200; 640 strips 92 and 99,
+// 292 and 368; I 512, 16 slots, 61.5 and 64.7; I 1024, 8 experts, 12 slots, 47.9 and
+// 49.6).  The layer in us, 64 experts for 1 and 4 tokens to 8 each, 128 for more, one
+// strip a workgroup and two:
 //   strips  1 token, I 768   4 tokens, I 2048   23 tokens, I 768   64 tokens, I 768
 //     128     11.6   12.6       51.6   57.9        70.6   81.0       136    157
 //     256     12.6   13.6       59.8   66.1        81.9   92.0       153    174
+//     272     14.1   13.9       78.1   70.0       114.4   97.6       222    182
 //     368     14.9   14.5       86.3   77.6       127.0  108.8       244    202
 //     512     16.7   16.3      100.2   91.9       149.2  130.8       283    242
 //     640     20.6   22.1      131.8  132.1       198.7  195.3       382    372
@@ -763,7 +770,7 @@ hipError_t launch_four(Few p, hipStream_t stream) {
   auto* down = p.tokens <= 16 ? few_down_kernel<FOUR, 16, 1> : few_down_kernel<FOUR, kMaxTokens, 1>;
   unsigned groups = (unsigned)strips<FOUR>(p.hidden);
   if constexpr (FOUR) {
-    if (groups > kDownAlone) {
+    if (groups > kDownAlone && slots <= (int64_t)kDownCrowd * p.num_groups) {
       down = p.tokens <= 16 ? few_down_kernel<FOUR, 16, 2> : few_down_kernel<FOUR, kMaxTokens, 2>;
       groups /= 2;
     }

@@ -79,11 +79,11 @@ def test_strips_cover_the_rule():
 
 
 @pytest.mark.parametrize("four", [False, True])
-@pytest.mark.parametrize("tokens,topk,experts", [(1, 8, 16), (19, 3, 10), (64, 2, 7)])
+@pytest.mark.parametrize("tokens,topk,experts", [(1, 8, 16), (19, 3, 10), (20, 2, 5), (41, 1, 5), (64, 2, 7)])
 @pytest.mark.parametrize("hidden", [2016, 2048, 2080, 2880, 4096])
 def test_widths_around_a_strip_for_each_compute_unit(four, tokens, topk, experts, hidden):
     """4 bits: 256 strips of the down product and the next more, where workgroups
-    begin to take two; a last span that is not full."""
+    begin to take two, up to 8 slots an expert; a last span that is not full."""
     device()
     layer = exact.Layer(four, experts, hidden, 288, topk, seed=hidden)
     x, ids, weights = exact.inputs(hidden, tokens, hidden, exact.some_experts(tokens, tokens, topk, experts, 0.1))
